@@ -16,10 +16,12 @@ Python ints; a non-zero status raises :class:`SkinnyError`):
     skinny_gemm_status_string, skinny_gemm_version,
     skinny_gemm_split_k_workspace_bytes, skinny_gemm_bf16_split_k,
     skinny_gemm_bf16_split_k_noalloc, skinny_gemm_split_k_num_variants,
-    skinny_gemm_split_k_get_variant, skinny_gemm_split_k_default_plan
+    skinny_gemm_split_k_get_variant, skinny_gemm_split_k_default_plan,
+    skinny_rms_norm_bf16, skinny_rms_norm_fp8, skinny_linear_bf16, skinny_linear_fp8
 
 Tensor helpers: :func:`gemm`, :func:`gemm_pair`, :func:`gemm_pair_strided`,
-:func:`split_k_workspace`, :func:`gemm_split_k` and :func:`gemm_split_k_noalloc`.
+:func:`split_k_workspace`, :func:`gemm_split_k` and :func:`gemm_split_k_noalloc`;
+:func:`rms_norm` and :func:`linear` (any number of rows, ``include/skinny_ops.h``).
 """
 from __future__ import annotations
 
@@ -44,6 +46,18 @@ SKINNY_KIND_LOOP_K = 2
 SKINNY_KIND_SCALAR = 3
 SKINNY_KIND_MFMA = 4
 SKINNY_KIND_SPLIT_K = 5
+
+SKINNY_ACT_NONE = 0
+SKINNY_ACT_RELU = 1
+SKINNY_ACT_GELU = 2
+SKINNY_ACT_GELU_TANH = 3
+SKINNY_ACT_SILU = 4
+
+SKINNY_SCALES_ROW = 1
+SKINNY_SCALES_BLOCK = 2
+
+ACTS = {"none": SKINNY_ACT_NONE, "relu": SKINNY_ACT_RELU, "gelu": SKINNY_ACT_GELU,
+        "gelu_tanh": SKINNY_ACT_GELU_TANH, "silu": SKINNY_ACT_SILU}
 
 
 class SkinnyError(RuntimeError):
@@ -77,6 +91,32 @@ class Plan(ctypes.Structure):
 
     def __repr__(self) -> str:
         return "Plan(" + ", ".join(f"{k}={v}" for k, v in self.as_dict().items()) + ")"
+
+
+class NormArgs(ctypes.Structure):
+    """skinny_norm_t."""
+
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+        ("residual_out", ctypes.c_void_p), ("y", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+        ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldro", ctypes.c_int64),
+        ("ldy", ctypes.c_int64), ("M", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("group", ctypes.c_int32), ("eps", ctypes.c_float),
+    ]
+
+
+class LinearArgs(ctypes.Structure):
+    """skinny_linear_t."""
+
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("W0", ctypes.c_void_p), ("W1", ctypes.c_void_p),
+        ("x_scale", ctypes.c_void_p), ("w0_scale", ctypes.c_void_p), ("w1_scale", ctypes.c_void_p),
+        ("bias0", ctypes.c_void_p), ("bias1", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+        ("y", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64),
+        ("ldy", ctypes.c_int64), ("M", ctypes.c_int32), ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32), ("act", ctypes.c_int32), ("out_f32", ctypes.c_int32),
+        ("scales", ctypes.c_int32),
+    ]
 
 
 _lock = threading.Lock()
@@ -118,6 +158,10 @@ def lib() -> ctypes.CDLL:
         L.skinny_gemm_split_k_num_variants.argtypes = []
         L.skinny_gemm_split_k_get_variant.argtypes = [i, pp]
         L.skinny_gemm_split_k_default_plan.argtypes = [i, i, i, pp]
+        for name, args in (("skinny_rms_norm_bf16", NormArgs), ("skinny_rms_norm_fp8", NormArgs),
+                           ("skinny_linear_bf16", LinearArgs), ("skinny_linear_fp8", LinearArgs)):
+            getattr(L, name).argtypes = [ctypes.POINTER(args), vp]
+            getattr(L, name).restype = ctypes.c_int
         for name in ("skinny_gemm_init", "skinny_gemm_bf16", "skinny_gemm_bf16_pair",
                      "skinny_gemm_bf16_ex", "skinny_gemm_bf16_pair_ex", "skinny_gemm_bf16_f32out",
                      "skinny_gemm_bf16_f32out_ex", "skinny_gemm_bf16_pair_strided",
@@ -265,6 +309,22 @@ def skinny_gemm_split_k_default_plan(M: int, N: int, K: int) -> Plan:
 
 def split_k_variants() -> list[Plan]:
     return [skinny_gemm_split_k_get_variant(i) for i in range(skinny_gemm_split_k_num_variants())]
+
+
+def skinny_rms_norm_bf16(args: NormArgs, stream: int = 0) -> None:
+    _check(lib().skinny_rms_norm_bf16(ctypes.byref(args), stream), "skinny_rms_norm_bf16")
+
+
+def skinny_rms_norm_fp8(args: NormArgs, stream: int = 0) -> None:
+    _check(lib().skinny_rms_norm_fp8(ctypes.byref(args), stream), "skinny_rms_norm_fp8")
+
+
+def skinny_linear_bf16(args: LinearArgs, stream: int = 0) -> None:
+    _check(lib().skinny_linear_bf16(ctypes.byref(args), stream), "skinny_linear_bf16")
+
+
+def skinny_linear_fp8(args: LinearArgs, stream: int = 0) -> None:
+    _check(lib().skinny_linear_fp8(ctypes.byref(args), stream), "skinny_linear_fp8")
 
 
 # ---- tensor helpers ---------------------------------------------------------
@@ -494,6 +554,148 @@ def gemm_split_k_noalloc(x: torch.Tensor, W: torch.Tensor, plan: Plan | None = N
     return out
 
 
+def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device,
+            shape: tuple | None = None) -> int:
+    """Check a 2-D row-strided GPU matrix and return its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be on {device or 'a GPU'}, got {t.device}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be {list(shape) if shape else '2-D'}, got {list(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride, got stride {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(t: torch.Tensor | None, name: str, dtype: torch.dtype, device: torch.device,
+            shape: tuple) -> int | None:
+    """Check an optional contiguous GPU tensor and return its address."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on {device}, got "
+                         f"{list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+             residual: torch.Tensor | None = None, quant: str | None = None,
+             out: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+             residual_out: torch.Tensor | None = None):
+    """Root-mean-square norm of x [M, D] (rows may be strided), or of x + residual:
+    y = h * weight / sqrt(mean(h^2) + eps), one kernel launch on the current stream.
+
+    quant None: y is bfloat16. quant "row" or "group": y is float8_e4m3fn with float32
+    scales per row ([M]) or per 128 columns ([M, ceil(D / 128)]). Returns y, or (y, scale)
+    with quant; with a residual the new residual h (bfloat16) is returned last. out, scale
+    and residual_out may be given; residual_out may be residual or x, and out may be x."""
+    ldx = _matrix(x, "x", torch.bfloat16, None)
+    M, D = x.shape
+    if quant not in (None, "row", "group"):
+        raise ValueError(f"quant must be None, 'row' or 'group', got {quant!r}")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if quant is None and scale is not None:
+        raise ValueError("scale needs quant")
+    a = NormArgs(x=x.data_ptr(), ldx=ldx, M=M, D=D, eps=eps, group=128 if quant == "group" else 0)
+    a.weight = _vector(weight, "weight", torch.bfloat16, x.device, (D,))
+    if weight is None:
+        raise TypeError("weight must be a torch.Tensor")
+    dtype = torch.bfloat16 if quant is None else torch.float8_e4m3fn
+    if out is None:
+        out = torch.empty((M, D), dtype=dtype, device=x.device)
+    a.ldy = _matrix(out, "out", dtype, x.device, (M, D))
+    a.y = out.data_ptr()
+    if residual is not None:
+        a.ldr = _matrix(residual, "residual", torch.bfloat16, x.device, (M, D))
+        a.residual = residual.data_ptr()
+        if residual_out is None:
+            residual_out = torch.empty((M, D), dtype=torch.bfloat16, device=x.device)
+        a.ldro = _matrix(residual_out, "residual_out", torch.bfloat16, x.device, (M, D))
+        a.residual_out = residual_out.data_ptr()
+    got = [out]
+    if quant is not None:
+        shape = (M,) if quant == "row" else (M, -(-D // 128))
+        if scale is None:
+            scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+        a.scale = _vector(scale, "scale", torch.float32, x.device, shape)
+        got.append(scale)
+    if residual is not None:
+        got.append(residual_out)
+    s = _stream_handle(x.device)
+    with _on_device(x.device):
+        (skinny_rms_norm_bf16 if quant is None else skinny_rms_norm_fp8)(a, s)
+    return got[0] if len(got) == 1 else tuple(got)
+
+
+def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None,
+           residual: torch.Tensor | None = None, act: str = "none",
+           W_up: torch.Tensor | None = None, bias_up: torch.Tensor | None = None,
+           x_scale: torch.Tensor | None = None, w_scale: torch.Tensor | None = None,
+           w_up_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+           out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """y = act(x @ W.T + bias) + residual for any number of rows of x [M, K] (rows may be
+    strided), or the gated form act(x @ W.T + bias) * (x @ W_up.T + bias_up); one kernel
+    launch on the current stream.
+
+    x and W are bfloat16, or float8_e4m3fn with float32 scales: per row (x_scale [M],
+    w_scale [N]) or per 128 columns of x and 128 x 128 block of W (x_scale
+    [M, ceil(K/128)], w_scale [ceil(N/128), ceil(K/128)]). act: none, relu, gelu,
+    gelu_tanh or silu. out may be given; a bfloat16 out may be the residual itself."""
+    fp8 = isinstance(x, torch.Tensor) and x.dtype == torch.float8_e4m3fn
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    ldx = _matrix(x, "x", dtype, None)
+    M, K = x.shape
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    _matrix(W, "W", dtype, x.device)
+    N = W.shape[0]
+    if tuple(W.shape) != (N, K):
+        raise ValueError(f"inner sizes differ: x {tuple(x.shape)}, W {tuple(W.shape)}")
+    if W_up is None and bias_up is not None:
+        raise ValueError("bias_up needs W_up")
+    if W_up is not None and residual is not None:
+        raise ValueError("the gated form takes no residual")
+    if W_up is not None and N * K == 0 and M > 0:
+        raise ValueError("the gated form needs N and K above 0")
+    if not fp8 and not (x_scale is None and w_scale is None and w_up_scale is None):
+        raise ValueError("scales belong to float8_e4m3fn inputs")
+    a = LinearArgs(x=x.data_ptr(), ldx=ldx, M=M, N=N, K=K, act=ACTS[act],
+                   out_f32=out_dtype == torch.float32)
+    a.W0 = _vector(W, "W", dtype, x.device, (N, K))
+    a.W1 = _vector(W_up, "W_up", dtype, x.device, (N, K))
+    a.bias0 = _vector(bias, "bias", torch.bfloat16, x.device, (N,))
+    a.bias1 = _vector(bias_up, "bias_up", torch.bfloat16, x.device, (N,))
+    if fp8:
+        if x_scale is None or w_scale is None or (W_up is not None) != (w_up_scale is not None):
+            raise ValueError("float8_e4m3fn inputs need x_scale and a scale for each weight")
+        blocks = w_scale.dim() == 2
+        kb, nb = -(-K // 128), -(-N // 128)
+        a.scales = SKINNY_SCALES_BLOCK if blocks else SKINNY_SCALES_ROW
+        ws = (nb, kb) if blocks else (N,)
+        a.x_scale = _vector(x_scale, "x_scale", torch.float32, x.device, (M, kb) if blocks else (M,))
+        a.w0_scale = _vector(w_scale, "w_scale", torch.float32, x.device, ws)
+        a.w1_scale = _vector(w_up_scale, "w_up_scale", torch.float32, x.device, ws)
+    if residual is not None:
+        a.ldr = _matrix(residual, "residual", torch.bfloat16, x.device, (M, N))
+        a.residual = residual.data_ptr()
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    a.ldy = _matrix(out, "out", out_dtype, x.device, (M, N))
+    a.y = out.data_ptr()
+    s = _stream_handle(x.device)
+    with _on_device(x.device):
+        (skinny_linear_fp8 if fp8 else skinny_linear_bf16)(a, s)
+    return out
+
+
 __all__ = [
     "SkinnyError", "Plan", "lib", "variants", "gemm", "gemm_pair", "gemm_pair_strided",
     "split_k_variants", "split_k_workspace", "gemm_split_k", "gemm_split_k_noalloc",
@@ -507,5 +709,8 @@ __all__ = [
     "skinny_gemm_get_variant", "skinny_gemm_status_string", "skinny_gemm_version",
     "SKINNY_OK", "SKINNY_ERR_INVALID_ARG", "SKINNY_ERR_UNSUPPORTED", "SKINNY_ERR_NOT_INITIALIZED",
     "SKINNY_ERR_LAUNCH", "SKINNY_KIND_FIXED_K", "SKINNY_KIND_LOOP_K", "SKINNY_KIND_SCALAR",
-    "SKINNY_KIND_MFMA",
+    "SKINNY_KIND_MFMA", "NormArgs", "LinearArgs", "ACTS", "rms_norm", "linear",
+    "skinny_rms_norm_bf16", "skinny_rms_norm_fp8", "skinny_linear_bf16", "skinny_linear_fp8",
+    "SKINNY_ACT_NONE", "SKINNY_ACT_RELU", "SKINNY_ACT_GELU", "SKINNY_ACT_GELU_TANH",
+    "SKINNY_ACT_SILU", "SKINNY_SCALES_ROW", "SKINNY_SCALES_BLOCK",
 ]

@@ -1,0 +1,185 @@
+// Host side of skinny_linear_bf16 / skinny_linear_fp8 (include/skinny_ops.h): the choice
+// of kernel, and the element-wise kernel for what the vector paths do not take.
+#include "ops_host.hpp"
+
+#include <cstdint>
+
+#include "linear.hpp"
+#include "linear_tile.hpp"
+#include "validate_ops.hpp"
+
+namespace skg {
+
+// Any alignment, stride and K: 16 x 16 outputs per block of 256 threads, K in parts of
+// 64 columns through LDS as floats (64 divides a 128-column block of scales).
+template <int MODE, bool GATED>
+__global__ __launch_bounds__(256) void linear_any_kernel(LinArgs a, int64_t tiles, int nt)
+{
+    constexpr int MATS = GATED ? 2 : 1;
+    __shared__ float xl[16][65], wl[MATS][16][65];
+    const int tn = threadIdx.x & 15, tm = threadIdx.x >> 4;
+    const int64_t wld = (int64_t)a.K;
+    auto at = [&](const uint8_t *p, int64_t i) {
+        if constexpr (MODE == 0)
+            return bf16_to_f32(reinterpret_cast<const uint16_t *>(p)[i]);
+        else
+            return __builtin_amdgcn_cvt_f32_fp8((int)p[i], 0);
+    };
+    const int64_t ldx = MODE == 0 ? a.ldx / 2 : a.ldx;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int n0 = (int)(tile % nt) * 16, m0 = (int)(tile / nt) * 16;
+        float acc[MATS] = {};
+        for (int k0 = 0; k0 < a.K; k0 += 64) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < 16 * 64; i += 256) {
+                const int r = i >> 6, k = i & 63;
+                const bool kin = k < a.K - k0;
+                xl[r][k] = kin && r < a.M - m0 ? at(a.x, (int64_t)(m0 + r) * ldx + k0 + k) : 0.0f;
+#pragma unroll
+                for (int t = 0; t < MATS; ++t)
+                    wl[t][r][k] = kin && r < a.N - n0 ? at(a.w[t], (int64_t)(n0 + r) * wld + k0 + k) : 0.0f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int t = 0; t < MATS; ++t) {
+                float p = MODE == 2 ? 0.0f : acc[t];
+                for (int k = 0; k < 64; ++k)
+                    p = __builtin_fmaf(xl[tm][k], wl[t][tn][k], p);
+                if constexpr (MODE == 2) {
+                    const int b = k0 >> 7;
+                    if (tm < a.M - m0 && tn < a.N - n0)
+                        acc[t] = __builtin_fmaf(p, a.xs[(int64_t)(m0 + tm) * a.kb + b] *
+                                                       a.ws[t][(int64_t)((n0 + tn) >> 7) * a.kb + b], acc[t]);
+                } else {
+                    acc[t] = p;
+                }
+            }
+            if (k0 > 0x7FFFFFFF - 64)
+                break;  // the next k0 would pass 32 bits
+        }
+        if (tm < a.M - m0 && tn < a.N - n0) {
+            const int m = m0 + tm, n = n0 + tn;
+            float v[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int t = 0; t < MATS; ++t) {
+                v[t] = acc[t];
+                if constexpr (MODE == 1)
+                    if (a.K > 0)
+                        v[t] *= a.xs[m] * a.ws[t][n];
+            }
+            put(a, finish<GATED>(a, v[0], v[1], m, n), m, n);
+        }
+    }
+}
+
+}  // namespace skg
+
+namespace skg_host {
+namespace {
+
+const void *any_fn(int mode, bool gated)
+{
+    using namespace skg;
+    static const void *const fn[3][2] = {
+        {(const void *)&linear_any_kernel<0, false>, (const void *)&linear_any_kernel<0, true>},
+        {(const void *)&linear_any_kernel<1, false>, (const void *)&linear_any_kernel<1, true>},
+        {(const void *)&linear_any_kernel<2, false>, (const void *)&linear_any_kernel<2, true>}};
+    return fn[mode][gated];
+}
+
+// A launch holds fewer than 2^32 threads; blocks here have at most 512.
+constexpr int64_t kMaxBlocks = 1 << 22;
+
+int run_linear(const skinny_linear_t *p, bool fp8, hipStream_t stream)
+{
+    int st = validate_linear(p, fp8);
+    if (st != SKINNY_OK || p->M == 0 || p->N == 0)
+        return st;
+    int cus = 0;
+    st = ops_device(&cus);
+    if (st != SKINNY_OK)
+        return st;
+    const int mode = p->scales;  // 0 bfloat16, 1 row, 2 block
+    const bool gated = p->W1 != nullptr;
+    skg::LinArgs a{};
+    a.x = static_cast<const uint8_t *>(p->x);
+    a.w[0] = static_cast<const uint8_t *>(p->W0);
+    a.w[1] = static_cast<const uint8_t *>(p->W1);
+    a.xs = p->x_scale;
+    a.ws[0] = p->w0_scale;
+    a.ws[1] = p->w1_scale;
+    a.bias[0] = static_cast<const uint16_t *>(p->bias0);
+    a.bias[1] = static_cast<const uint16_t *>(p->bias1);
+    a.res = static_cast<const uint16_t *>(p->residual);
+    a.y = p->y;
+    a.ldx = p->ldx * (fp8 ? 1 : 2);
+    a.ldr = p->ldr;
+    a.ldy = p->ldy;
+    a.M = p->M;
+    a.N = p->N;
+    a.K = p->K;
+    a.kb = (int)(((int64_t)p->K + 127) / 128);
+    a.act = p->act;
+    a.out_f32 = p->out_f32;
+
+    // the element-wise kernel loops over its tiles, so it takes any size
+    auto launch_any = [&]() {
+        int nt = (int)(((int64_t)a.N + 15) / 16);
+        int64_t tiles = (((int64_t)a.M + 15) / 16) * nt;
+        void *args[] = {&a, &tiles, &nt};
+        return ops_launch(any_fn(mode, gated), dim3((unsigned)(tiles < (1 << 20) ? tiles : 1 << 20)), 256, args,
+                          stream);
+    };
+    if (!linear_vector_ok(*p, fp8))
+        return launch_any();
+    const bool exact = a.out_f32 != 0;
+    const int small_most = gated ? 32 : 64;
+    if (a.M <= small_most) {
+        const int nr = 1;
+        const SmallKernel k = mode == 0   ? small_kernel_bf16(a.M, gated, nr, exact)
+                              : mode == 1 ? small_kernel_row(a.M, gated, nr, exact)
+                                          : small_kernel_block(a.M, gated, nr, exact);
+        const int units = (int)(((int64_t)a.K * (fp8 ? 1 : 2) + k.unit_bytes - 1) / k.unit_bytes);
+        int waves = 8;
+        while (waves > 1 && units < waves * k.depth)
+            waves /= 2;
+        const int64_t blocks = ((int64_t)a.N + k.rows - 1) / k.rows;
+        if (blocks > kMaxBlocks)
+            return launch_any();
+        void *args[] = {&a};
+        return ops_launch(k.fn, dim3((unsigned)blocks), waves * 64, args, stream);
+    }
+    // the largest tile that still gives every compute unit a block
+    TileKernel k{};
+    int64_t nt = 0, mt = 0;
+    for (int size = 2; size >= 0; --size) {
+        k = mode == 0 ? tile_kernel_bf16(gated, exact, size) : mode == 1 ? tile_kernel_row(gated, exact, size)
+                                                                  : tile_kernel_block(gated, exact, size);
+        nt = ((int64_t)a.N + k.bn - 1) / k.bn;
+        mt = ((int64_t)a.M + k.bm - 1) / k.bm;
+        if (nt * mt >= cus)
+            break;
+    }
+    if (nt * mt > kMaxBlocks)
+        return launch_any();
+    int nti = (int)nt, mti = (int)mt;
+    void *args[] = {&a, &nti, &mti};
+    return ops_launch(k.fn, dim3((unsigned)(nt * mt)), k.threads, args, stream);
+}
+
+}  // namespace
+}  // namespace skg_host
+
+extern "C" {
+
+int skinny_linear_bf16(const skinny_linear_t *args, hipStream_t stream)
+{
+    return skg_host::run_linear(args, false, stream);
+}
+
+int skinny_linear_fp8(const skinny_linear_t *args, hipStream_t stream)
+{
+    return skg_host::run_linear(args, true, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,11 @@
+// The few-row projection kernels of one element type and scale mode.
+#include "linear_small.hpp"
+
+namespace skg_host {
+
+SmallKernel small_kernel_row(int M, bool gated, int nr, bool exact)
+{
+    return small_pick<1>(M, gated, nr, exact);
+}
+
+}  // namespace skg_host

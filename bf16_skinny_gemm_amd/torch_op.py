@@ -17,7 +17,12 @@ linear path otherwise. Here:
 * :func:`skinny_linear` routes: qualifying calls go to the op, others to
   ``torch.nn.functional.linear`` only when ``fallback=True`` (the default for the
   module hook), else they raise;
-* :func:`install` swaps the forward of ``nn.Linear`` modules for the routed one.
+* :func:`install` swaps the forward of ``nn.Linear`` modules for the routed one;
+* ``rms_norm``, ``add_rms_norm``, ``rms_norm_fp8``, ``add_rms_norm_fp8``, ``linear_act``,
+  ``linear_gated``, ``linear_fp8`` and ``linear_gated_fp8`` (``torch.ops.skinny.*``, same
+  registration) are the operators around the projection, for any number of rows;
+  :func:`install` with ``fused=True`` routes biased ``nn.Linear`` layers and
+  ``nn.RMSNorm`` modules to them.
 
 A call qualifies when x and weight are bfloat16 CUDA tensors on a gfx950 device,
 weight is [N, K] contiguous, x is [..., K] with 1 <= prod(leading dims) <= 8
@@ -34,6 +39,8 @@ import os
 import torch
 
 from . import _on_device, _stream_handle, lib, skinny_gemm_bf16
+from . import linear as _linear_call
+from . import rms_norm as _norm_call
 from .build import TORCH_OP_PATH
 
 _ARCH_OK: dict[int, bool] = {}
@@ -118,6 +125,123 @@ torch.library.register_fake("skinny::linear", _linear_fake, lib=_LIB)
 linear = torch.ops.skinny.linear
 
 
+# ---- the operators around the projection ------------------------------------
+
+_SCHEMAS = (
+    "rms_norm(Tensor x, Tensor weight, float eps) -> Tensor",
+    "add_rms_norm(Tensor x, Tensor residual, Tensor weight, float eps) -> (Tensor, Tensor)",
+    "rms_norm_fp8(Tensor x, Tensor weight, float eps, int group) -> (Tensor, Tensor)",
+    "add_rms_norm_fp8(Tensor x, Tensor residual, Tensor weight, float eps, int group) "
+    "-> (Tensor, Tensor, Tensor)",
+    "linear_act(Tensor x, Tensor weight, Tensor? bias=None, Tensor? residual=None, "
+    "str act='none', bool out_f32=False) -> Tensor",
+    "linear_gated(Tensor x, Tensor w_gate, Tensor w_up, Tensor? b_gate=None, Tensor? b_up=None, "
+    "str act='silu', bool out_f32=False) -> Tensor",
+    "linear_fp8(Tensor x, Tensor x_scale, Tensor weight, Tensor w_scale, Tensor? bias=None, "
+    "Tensor? residual=None, str act='none', bool out_f32=False) -> Tensor",
+    "linear_gated_fp8(Tensor x, Tensor x_scale, Tensor w_gate, Tensor gate_scale, Tensor w_up, "
+    "Tensor up_scale, Tensor? b_gate=None, Tensor? b_up=None, str act='silu', "
+    "bool out_f32=False) -> Tensor",
+)
+
+
+def _quant(group: int) -> str:
+    if group not in (0, 128):
+        raise ValueError(f"group must be 0 (per row) or 128, got {group}")
+    return "group" if group else "row"
+
+
+def _scale_shape(x: torch.Tensor, group: int) -> tuple:
+    return (*x.shape[:-1], -(-x.shape[-1] // 128)) if group else tuple(x.shape[:-1])
+
+
+def _norm_py(x, weight, eps, residual=None, quant=None):
+    """Python kernels of the norms (used when the C++ operators are not built)."""
+    D = x.shape[-1]
+    got = _norm_call(x.reshape(-1, D), weight, eps,
+                     residual=None if residual is None else residual.reshape(-1, D), quant=quant)
+    got = got if isinstance(got, tuple) else (got,)
+    shapes = [x.shape] + ([_scale_shape(x, quant == "group")] if quant else []) + [x.shape]
+    got = tuple(g.reshape(s) for g, s in zip(got, shapes))
+    return got[0] if len(got) == 1 else got
+
+
+def _linear_py(x, weight, bias, residual, act, out_f32, W_up=None, bias_up=None, x_scale=None,
+               w_scale=None, w_up_scale=None):
+    """Python kernels of the projections (used when the C++ operators are not built)."""
+    K, N = x.shape[-1], weight.shape[0]
+    if x_scale is not None:
+        x_scale = x_scale.reshape(-1) if w_scale.dim() == 1 else x_scale.reshape(-1, x_scale.shape[-1])
+    y = _linear_call(x.reshape(-1, K), weight, bias=bias, act=act, W_up=W_up, bias_up=bias_up,
+                     residual=None if residual is None else residual.reshape(-1, N),
+                     x_scale=x_scale, w_scale=w_scale, w_up_scale=w_up_scale,
+                     out_dtype=torch.float32 if out_f32 else torch.bfloat16)
+    return y.reshape(*x.shape[:-1], N)
+
+
+_PY_KERNELS = {
+    "rms_norm": lambda x, w, eps: _norm_py(x, w, eps),
+    "add_rms_norm": lambda x, r, w, eps: _norm_py(x, w, eps, r),
+    "rms_norm_fp8": lambda x, w, eps, group: _norm_py(x, w, eps, None, _quant(group)),
+    "add_rms_norm_fp8": lambda x, r, w, eps, group: _norm_py(x, w, eps, r, _quant(group)),
+    "linear_act": lambda x, w, b=None, r=None, act="none", f32=False: _linear_py(x, w, b, r, act, f32),
+    "linear_gated": lambda x, w, u, b=None, bu=None, act="silu", f32=False: _linear_py(
+        x, w, b, None, act, f32, u, bu),
+    "linear_fp8": lambda x, xs, w, ws, b=None, r=None, act="none", f32=False: _linear_py(
+        x, w, b, r, act, f32, x_scale=xs, w_scale=ws),
+    "linear_gated_fp8": lambda x, xs, w, ws, u, us, b=None, bu=None, act="silu", f32=False: _linear_py(
+        x, w, b, None, act, f32, u, bu, xs, ws, us),
+}
+
+
+def _refuse_cpu(name):
+    def refuse(*args, **kwargs):
+        raise ValueError(f"skinny::{name}: runs on gfx950 GPU tensors only")
+    return refuse
+
+
+def _y_fake(x, n, f32):
+    return x.new_empty((*x.shape[:-1], n), dtype=torch.float32 if f32 else torch.bfloat16)
+
+
+def _q_fake(x, group):
+    _quant(group)
+    return (x.new_empty(x.shape, dtype=torch.float8_e4m3fn),
+            x.new_empty(_scale_shape(x, group), dtype=torch.float32))
+
+
+_FAKES = {
+    "rms_norm": lambda x, weight, eps: x.new_empty(x.shape),
+    "add_rms_norm": lambda x, residual, weight, eps: (x.new_empty(x.shape), x.new_empty(x.shape)),
+    "rms_norm_fp8": lambda x, weight, eps, group: _q_fake(x, group),
+    "add_rms_norm_fp8": lambda x, residual, weight, eps, group: (*_q_fake(x, group), x.new_empty(x.shape)),
+    "linear_act": lambda x, weight, bias=None, residual=None, act="none", out_f32=False: _y_fake(
+        x, weight.shape[0], out_f32),
+    "linear_gated": lambda x, w_gate, w_up, b_gate=None, b_up=None, act="silu", out_f32=False: _y_fake(
+        x, w_gate.shape[0], out_f32),
+    "linear_fp8": lambda x, x_scale, weight, w_scale, bias=None, residual=None, act="none",
+    out_f32=False: _y_fake(x, weight.shape[0], out_f32),
+    "linear_gated_fp8": lambda x, x_scale, w_gate, gate_scale, w_up, up_scale, b_gate=None, b_up=None,
+    act="silu", out_f32=False: _y_fake(x, w_gate.shape[0], out_f32),
+}
+
+for _schema in _SCHEMAS:
+    _name = _schema.split("(")[0]
+    if not CPP_OP:
+        _LIB.define(_schema)
+        _LIB.impl(_name, _PY_KERNELS[_name], "CUDA")
+        _LIB.impl(_name, _refuse_cpu(_name), "CPU")
+    torch.library.register_fake("skinny::" + _name, _FAKES[_name], lib=_LIB)
+rms_norm = torch.ops.skinny.rms_norm.default
+add_rms_norm = torch.ops.skinny.add_rms_norm.default
+rms_norm_fp8 = torch.ops.skinny.rms_norm_fp8.default
+add_rms_norm_fp8 = torch.ops.skinny.add_rms_norm_fp8.default
+linear_act = torch.ops.skinny.linear_act.default
+linear_gated = torch.ops.skinny.linear_gated.default
+linear_fp8 = torch.ops.skinny.linear_fp8.default
+linear_gated_fp8 = torch.ops.skinny.linear_gated_fp8.default
+
+
 def skinny_linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
                   fallback: bool = True) -> torch.Tensor:
     """F.linear semantics, routed: the skinny GEMM when the call qualifies,
@@ -129,18 +253,63 @@ def skinny_linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | No
     return torch.nn.functional.linear(x, weight, bias)
 
 
-def install(module: torch.nn.Module, fallback: bool = True) -> int:
+# Rows up to which a biased layer is routed: there linear_act reads each weight once, and
+# the standard path is a library product that serves larger batches well.
+FUSED_ROWS = 64
+
+
+def _inference(*tensors) -> bool:
+    """No gradient is asked for: the operators record none."""
+    return not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors))
+
+
+def qualifies_fused(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None) -> bool:
+    """True when a layer with (weight, bias) can run on linear_act."""
+    if x.dtype != torch.bfloat16 or x.device.type != "cuda" or x.dim() < 1 or x.numel() == 0:
+        return False
+    for t in (weight, bias):
+        if t is not None and (t.dtype != torch.bfloat16 or t.device != x.device or not t.is_contiguous()):
+            return False
+    if x.shape[-1] != weight.shape[1] or x.numel() // x.shape[-1] > FUSED_ROWS:
+        return False
+    return _inference(x, weight, bias) and _device_is_gfx950(x.device)
+
+
+def _norm_forward(self, x):
+    """nn.RMSNorm.forward on the HIP norm where it qualifies."""
+    w = self.weight
+    if (w is not None and w.dim() == 1 and x.dim() >= 1 and x.shape[-1] == w.shape[0] and x.numel() > 0
+            and x.dtype == w.dtype == torch.bfloat16 and x.device.type == "cuda" and w.device == x.device
+            and w.is_contiguous() and _inference(x, w) and _device_is_gfx950(x.device)):
+        eps = self.eps if self.eps is not None else torch.finfo(x.dtype).eps
+        return rms_norm(x, w, eps)
+    return type(self).forward(self, x)
+
+
+def install(module: torch.nn.Module, fallback: bool = True, fused: bool = False) -> int:
     """Route the forward of every nn.Linear inside ``module`` through
-    :func:`skinny_linear`. Returns the number of layers hooked."""
+    :func:`skinny_linear`. With ``fused``, layers with a bias and up to 64 rows of input
+    run on linear_act and nn.RMSNorm modules on rms_norm, both where no gradient is asked
+    for. Returns the number of modules hooked."""
     count = 0
     for sub in module.modules():
-        if isinstance(sub, torch.nn.Linear) and not getattr(sub, "_skinny_hooked", False):
-            def fwd(self, inp, _fallback=fallback):
+        if getattr(sub, "_skinny_hooked", False):
+            continue
+        if isinstance(sub, torch.nn.Linear):
+            def fwd(self, inp, _fallback=fallback, _fused=fused):
+                if _fused and self.bias is not None and qualifies_fused(inp, self.weight, self.bias):
+                    return linear_act(inp, self.weight, self.bias, None, "none", False)
                 return skinny_linear(inp, self.weight, self.bias, fallback=_fallback)
             sub.forward = functools.partial(fwd, sub)
-            sub._skinny_hooked = True
-            count += 1
+        elif fused and isinstance(sub, torch.nn.RMSNorm):
+            sub.forward = functools.partial(_norm_forward, sub)
+        else:
+            continue
+        sub._skinny_hooked = True
+        count += 1
     return count
 
 
-__all__ = ["linear", "skinny_linear", "install", "qualifies", "CPP_OP"]
+__all__ = ["linear", "skinny_linear", "install", "qualifies", "qualifies_fused", "CPP_OP", "FUSED_ROWS",
+           "rms_norm", "add_rms_norm", "rms_norm_fp8", "add_rms_norm_fp8", "linear_act", "linear_gated",
+           "linear_fp8", "linear_gated_fp8"]

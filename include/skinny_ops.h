@@ -1,0 +1,125 @@
+/*
+ * skinny_ops.h -- C ABI of the operators around the skinny GEMM, in the same library
+ * (libskinny_gemm_bf16.so): the norm in front of a projection, and projections whose
+ * bias, activation, gate and residual are applied before the result is stored, on
+ * bfloat16 or on 8-bit floats with scales.
+ *
+ * Conventions shared by every entry point below:
+ *  - Pointers are DEVICE pointers. bfloat16 and e4m3 values (the OCP 8-bit float
+ *    with 4 exponent and 3 fraction bits, largest value 448, no infinities) are
+ *    raw bit patterns. Matrices are row-major; ld* is a row stride in elements.
+ *  - M, the number of rows of x, is any value from 0 up: one decode token or a
+ *    whole prompt. M == 0, N == 0 or D == 0 is a no-op that returns SKINNY_OK.
+ *  - The caller owns every buffer. A call enqueues exactly one kernel on `stream`
+ *    of the current device and returns: no allocation, no synchronisation, no
+ *    workspace, no state kept between calls. Calls are legal under HIP graph
+ *    capture, and calls on different streams may overlap.
+ *  - Arguments are checked before anything is enqueued. Nothing is written on
+ *    error, and nothing outside the named rows and columns ever is: the columns
+ *    between the width and the row stride stay as they were.
+ *  - Sums, norms and activations are held in float32; each output value is rounded
+ *    once. Results depend on the inputs and sizes alone: the same call gives the same
+ *    bits, and no atomic is used.
+ *  - Only gfx950 devices are supported (others: SKINNY_ERR_UNSUPPORTED).
+ */
+#ifndef SKINNY_OPS_H
+#define SKINNY_OPS_H
+
+#include <stdint.h>
+
+#include "skinny_gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ---- Root-mean-square norm -----------------------------------------------------
+ *   h[m, d] = x[m, d] + residual[m, d]            (h = x without a residual)
+ *   y[m, d] = h[m, d] * weight[d] / sqrt(mean_d(h[m, d]^2) + eps)
+ * x, residual, weight: bfloat16. With a residual, h is also stored, rounded once to
+ * bfloat16, in residual_out; the norm is taken of the unrounded h. Squares are summed
+ * in float32, so they must stay finite (|h| below about 1e19 / sqrt(D)).
+ * residual and residual_out are both given or both NULL. residual_out may be residual
+ * or x itself (same pointer and stride), as may y be x in the bfloat16 form when
+ * residual_out is not x; no other overlap of an output with an input or another
+ * output is accepted. eps >= 0. Everything 2-byte aligned; any D and strides.
+ * Fast path: pointers 16-byte aligned, D and strides multiples of 8, D <= 32768;
+ * anything else runs an element-wise kernel.
+ */
+typedef struct skinny_norm {
+    const void *x;            /* [M][D] bfloat16, row stride ldx >= D */
+    const void *residual;     /* [M][D] bfloat16, row stride ldr, or NULL */
+    const void *weight;       /* [D] bfloat16 */
+    void *residual_out;       /* [M][D] bfloat16, row stride ldro, or NULL */
+    void *y;                  /* [M][D] bfloat16, or e4m3 for skinny_rms_norm_fp8; stride ldy */
+    float *scale;             /* skinny_rms_norm_fp8 only: [M] or [M][ceil(D / group)] */
+    int64_t ldx, ldr, ldro, ldy;
+    int32_t M, D;
+    int32_t group;            /* skinny_rms_norm_fp8: 0 = one scale per row, 128 = one per
+                                 128 columns; skinny_rms_norm_bf16: 0 */
+    float eps;
+} skinny_norm_t;
+
+/* y as bfloat16. */
+int skinny_rms_norm_bf16(const skinny_norm_t *args, hipStream_t stream);
+
+/* y as e4m3 with float32 scales: scale = max(largest |y| of the row or group, 2^-100)
+ * / 448 and q = e4m3(y / scale), nearest-even, so that q * scale stands for y. y is not
+ * rounded before that. A NaN in a row makes the row's scales and values NaN. An infinity makes
+ * the scale of its row or group NaN with all its values, and the row's other groups 0. */
+int skinny_rms_norm_fp8(const skinny_norm_t *args, hipStream_t stream);
+
+/* ---- Projections with an epilogue ----------------------------------------------
+ *   z[m, n] = sum_k x[m, k] * W0[n, k] + bias0[n]
+ *   y[m, n] = act(z[m, n]) + residual[m, n]
+ * and, with W1 given (the gated form; the residual is then NULL),
+ *   y[m, n] = act(z[m, n]) * (sum_k x[m, k] * W1[n, k] + bias1[n]).
+ * A merged gate/up weight [2N][K] is W0 = base, W1 = base + N * K elements.
+ * W0, W1: contiguous [N][K]. Biases and the residual are bfloat16, each optional.
+ * y may be the residual itself (bfloat16 output, same pointer and stride); no other
+ * overlap of y with an input is accepted. K == 0 gives act(bias) + residual.
+ * Fast path: x and W 16-byte aligned, row strides and K multiples of 16 bytes;
+ * anything else runs an element-wise kernel.
+ */
+typedef enum skinny_act {
+    SKINNY_ACT_NONE = 0,
+    SKINNY_ACT_RELU = 1,
+    SKINNY_ACT_GELU = 2,      /* z * Phi(z), with the error function */
+    SKINNY_ACT_GELU_TANH = 3, /* its tanh form: 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    SKINNY_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} skinny_act_t;
+
+typedef enum skinny_scales {
+    SKINNY_SCALES_ROW = 1,    /* x_scale [M], w_scale [N]: one per row of x and of W */
+    SKINNY_SCALES_BLOCK = 2   /* x_scale [M][ceil(K/128)], w_scale [ceil(N/128)][ceil(K/128)] */
+} skinny_scales_t;
+
+typedef struct skinny_linear {
+    const void *x;            /* [M][K], row stride ldx >= K */
+    const void *W0, *W1;      /* [N][K] contiguous; W1 NULL: not gated */
+    const float *x_scale;     /* skinny_linear_fp8 only, contiguous float32 (see skinny_scales) */
+    const float *w0_scale, *w1_scale;
+    const void *bias0, *bias1; /* [N] bfloat16 or NULL; bias1 only with W1 */
+    const void *residual;     /* [M][N] bfloat16, row stride ldr >= N, or NULL */
+    void *y;                  /* [M][N] bfloat16, or float32 with out_f32; row stride ldy >= N */
+    int64_t ldx, ldr, ldy;
+    int32_t M, N, K;
+    int32_t act;              /* skinny_act_t */
+    int32_t out_f32;          /* 0 or 1 */
+    int32_t scales;           /* skinny_linear_fp8: skinny_scales_t; skinny_linear_bf16: 0 */
+} skinny_linear_t;
+
+/* x and W bfloat16. */
+int skinny_linear_bf16(const skinny_linear_t *args, hipStream_t stream);
+
+/* x and W e4m3 with float32 scales: every product is multiplied by its x and W scale
+ * (per row: after the sum; per block: each 128-column part of the sum before it is
+ * added). The output of skinny_rms_norm_fp8 with group 0 or 128 is x with ROW or BLOCK
+ * scales. */
+int skinny_linear_fp8(const skinny_linear_t *args, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SKINNY_OPS_H */
