@@ -2,10 +2,10 @@
 // of kernel, and the element-wise kernel for what the vector paths do not take.
 #include "ops_host.hpp"
 
+#include <cmath>
 #include <cstdint>
 
 #include "linear.hpp"
-#include "linear_tile.hpp"
 #include "validate_ops.hpp"
 
 namespace skg {
@@ -90,6 +90,67 @@ const void *any_fn(int mode, bool gated)
 // A launch holds fewer than 2^32 threads; blocks here have at most 512.
 constexpr int64_t kMaxBlocks = 1 << 22;
 
+struct Choice {
+    const void *fn;
+    int64_t nt, mt;  // blocks along N and M
+    int waves;
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The kernel whose estimated time is least. The estimate of a streaming kernel has three
+// parts: the bytes of W and x once from HBM; the bytes that the fullest compute unit takes
+// into LDS; and the round trips its waves wait for one after another (a ring of two stages
+// hides a part of them). A part of all three is paid beside the largest, since they
+// overlap incompletely. That of a tiled kernel is its measured time per stage. The
+// constants were fitted to the times of 117 kernels at 583 sizes of each type (K 512 to
+// 8192, N 256 to 12576, M 1 to 4096): the choice takes 2.7% longer than the best of all
+// kernels on average, half of them within 0.5%.
+Choice choose(int mode, bool gated, bool exact, int M, int N, int64_t kbytes, int cus)
+{
+    const int mats = gated ? 2 : 1;
+    const double stages = (double)ceil_div(kbytes, 128);
+    const double hbm = ((double)mats * N + M) * (double)kbytes / 3.07e6;
+    Choice best{};
+    double least = 0.0;
+    auto offer = [&](const Choice &c, double us) {
+        if (!best.fn || us < least) {
+            best = c;
+            least = us;
+        }
+    };
+    StreamKernel s[kStreamMost];
+    const int ns = mode == 0   ? stream_kernels_bf16(M, gated, exact, s)
+                   : mode == 1 ? stream_kernels_row(M, gated, exact, s)
+                               : stream_kernels_block(M, gated, exact, s);
+    for (int i = 0; i < ns; ++i) {
+        const StreamKernel &k = s[i];
+        const Choice c{k.fn, ceil_div(N, k.nb), ceil_div(M, k.bm), k.waves};
+        const double per_cu = (double)ceil_div(c.nt * c.mt, cus);
+        double at_once = 163840 / k.lds < 32 / k.waves ? 163840 / k.lds : 32 / k.waves;
+        const double turns = std::ceil((double)(c.nt * c.mt) / (cus * at_once));
+        if (at_once > per_cu)
+            at_once = per_cu;
+        const double lds = per_cu * stages * k.stage / 86700.0;
+        const double trips = 0.276 * std::ceil(stages * per_cu / (k.waves * at_once * (1.0 + 1.2 * (k.ring - 1))));
+        double most = hbm > lds ? hbm : lds;
+        most = most > trips ? most : trips;
+        offer(c, 2.8 + most + 0.185 * (hbm + lds + trips) + turns * (1.0 + 0.025 * k.waves * k.tiles));
+    }
+    if (M <= 16)  // W once: a tile of many rows only adds work
+        return best;
+    TileKernel t[kTileMost];
+    const int ntk = mode == 0   ? tile_kernels_bf16(gated, exact, t)
+                    : mode == 1 ? tile_kernels_row(gated, exact, t)
+                                : tile_kernels_block(gated, exact, t);
+    for (int i = 0; i < ntk; ++i) {
+        const TileKernel &k = t[i];
+        const Choice c{k.fn, ceil_div(N, k.nb), ceil_div(M, k.bm), k.waves};
+        offer(c, 9.4 + stages * k.stage_us * (double)ceil_div(c.nt * c.mt, cus));
+    }
+    return best;
+}
+
 int run_linear(const skinny_linear_t *p, bool fp8, hipStream_t stream)
 {
     int st = validate_linear(p, fp8);
@@ -121,6 +182,7 @@ int run_linear(const skinny_linear_t *p, bool fp8, hipStream_t stream)
     a.kb = (int)(((int64_t)p->K + 127) / 128);
     a.act = p->act;
     a.out_f32 = p->out_f32;
+    a.vec4 = out4_ok(*p);
 
     // the element-wise kernel loops over its tiles, so it takes any size
     auto launch_any = [&]() {
@@ -132,39 +194,12 @@ int run_linear(const skinny_linear_t *p, bool fp8, hipStream_t stream)
     };
     if (!linear_vector_ok(*p, fp8))
         return launch_any();
-    const bool exact = a.out_f32 != 0;
-    const int small_most = gated ? 32 : 64;
-    if (a.M <= small_most) {
-        const int nr = 1;
-        const SmallKernel k = mode == 0   ? small_kernel_bf16(a.M, gated, nr, exact)
-                              : mode == 1 ? small_kernel_row(a.M, gated, nr, exact)
-                                          : small_kernel_block(a.M, gated, nr, exact);
-        const int units = (int)(((int64_t)a.K * (fp8 ? 1 : 2) + k.unit_bytes - 1) / k.unit_bytes);
-        int waves = 8;
-        while (waves > 1 && units < waves * k.depth)
-            waves /= 2;
-        const int64_t blocks = ((int64_t)a.N + k.rows - 1) / k.rows;
-        if (blocks > kMaxBlocks)
-            return launch_any();
-        void *args[] = {&a};
-        return ops_launch(k.fn, dim3((unsigned)blocks), waves * 64, args, stream);
-    }
-    // the largest tile that still gives every compute unit a block
-    TileKernel k{};
-    int64_t nt = 0, mt = 0;
-    for (int size = 2; size >= 0; --size) {
-        k = mode == 0 ? tile_kernel_bf16(gated, exact, size) : mode == 1 ? tile_kernel_row(gated, exact, size)
-                                                                  : tile_kernel_block(gated, exact, size);
-        nt = ((int64_t)a.N + k.bn - 1) / k.bn;
-        mt = ((int64_t)a.M + k.bm - 1) / k.bm;
-        if (nt * mt >= cus)
-            break;
-    }
-    if (nt * mt > kMaxBlocks)
+    const Choice c = choose(mode, gated, a.out_f32 != 0, a.M, a.N, (int64_t)a.K * (fp8 ? 1 : 2), cus);
+    if (c.nt * c.mt > kMaxBlocks)
         return launch_any();
-    int nti = (int)nt, mti = (int)mt;
-    void *args[] = {&a, &nti, &mti};
-    return ops_launch(k.fn, dim3((unsigned)(nt * mt)), k.threads, args, stream);
+    int nt = (int)c.nt, mt = (int)c.mt;
+    void *args[] = {&a, &nt, &mt};
+    return ops_launch(c.fn, dim3((unsigned)(c.nt * c.mt)), c.waves * 64, args, stream);
 }
 
 }  // namespace

@@ -5,7 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "kernels.hpp"
+#include "ops_device.hpp"
 #include "skinny_ops.h"
 
 namespace skg {
@@ -25,6 +25,7 @@ struct LinArgs {
     int M, N, K;               // K in elements
     int kb;                    // 128-column blocks of K (block scales)
     int act, out_f32;
+    int vec4;                  // four consecutive outputs, residuals and biases at a time
 };
 
 __device__ __forceinline__ float activate(float z, int act)
@@ -70,6 +71,72 @@ __device__ __forceinline__ void put(const LinArgs &a, float v, int m, int n)
         static_cast<float *>(a.y)[(int64_t)m * a.ldy + n] = v;
     else
         static_cast<uint16_t *>(a.y)[(int64_t)m * a.ldy + n] = f32_to_bf16(v);
+}
+
+// Four consecutive outputs n .. n + 3 of row m, from sums that their scales have yet to
+// multiply (MODE 1).
+template <int MODE, bool GATED>
+__device__ __forceinline__ void finish4(const LinArgs &a, f32x4 z, f32x4 u, int m, int n)
+{
+    if (a.vec4 && n + 4 <= a.N) {
+        if constexpr (MODE == 1) {
+            const float xs = a.xs[m];
+            const f32x4 s0 = *reinterpret_cast<const f32x4 *>(a.ws[0] + n);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                z[e] *= xs * s0[e];
+            if constexpr (GATED) {
+                const f32x4 s1 = *reinterpret_cast<const f32x4 *>(a.ws[1] + n);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    u[e] *= xs * s1[e];
+            }
+        }
+        if (a.bias[0]) {
+            const u32x2 b = *reinterpret_cast<const u32x2 *>(a.bias[0] + n);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                z[e] += e & 1 ? hi_f32(b[e >> 1]) : lo_f32(b[e >> 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            z[e] = activate(z[e], a.act);
+        if constexpr (GATED) {
+            if (a.bias[1]) {
+                const u32x2 b = *reinterpret_cast<const u32x2 *>(a.bias[1] + n);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    u[e] += e & 1 ? hi_f32(b[e >> 1]) : lo_f32(b[e >> 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                z[e] *= u[e];
+        } else if (a.res) {
+            const u32x2 r = *reinterpret_cast<const u32x2 *>(a.res + (int64_t)m * a.ldr + n);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                z[e] += e & 1 ? hi_f32(r[e >> 1]) : lo_f32(r[e >> 1]);
+        }
+        const int64_t at = (int64_t)m * a.ldy + n;
+        if (a.out_f32)
+            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.y) + at) = z;
+        else
+            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.y) + at) =
+                u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (n + e >= a.N)
+            continue;
+        float z1 = z[e], u1 = u[e];
+        if constexpr (MODE == 1) {
+            z1 *= a.xs[m] * a.ws[0][n + e];
+            if constexpr (GATED)
+                u1 *= a.xs[m] * a.ws[1][n + e];
+        }
+        put(a, finish<GATED>(a, z1, u1, m, n + e), m, n + e);
+    }
 }
 
 // D[i][j] += sum_k A[i][k] B[j][k] for 16 x 16 outputs. A lane holds, of its row
@@ -133,15 +200,29 @@ __device__ __forceinline__ f32x4 mfma_bytes(const u32x4 (&a)[2], const u32x4 (&b
 
 namespace skg_host {
 
-// Kernels of one element type and scale mode, by form. mode: 0 bfloat16, 1 row, 2 block.
-struct SmallKernel {
+// A kernel of linear_stream.hpp: outputs per block along N and M, stages per wave, waves,
+// bytes of a stage and of LDS, matrix instructions per stage.
+struct StreamKernel {
     const void *fn;
-    int rows;       // rows of W per block
-    int unit_bytes; // bytes of a row of W that one wave takes per step
-    int depth;      // steps in flight
+    int nb, bm, ring, waves, stage, lds, tiles;
 };
-SmallKernel small_kernel_bf16(int M, bool gated, int nr, bool exact);
-SmallKernel small_kernel_row(int M, bool gated, int nr, bool exact);
-SmallKernel small_kernel_block(int M, bool gated, int nr, bool exact);
+constexpr int kStreamMost = 8;  // kernels of one set
+
+// A kernel of linear_tile.hpp: outputs per block along N and M, waves, and a stage's time
+// (microseconds, blocks of one compute unit one after another).
+struct TileKernel {
+    const void *fn;
+    int nb, bm, waves;
+    float stage_us;
+};
+constexpr int kTileMost = 4;
+
+// The kernels that take M rows, by element type and scales; returns their number.
+int stream_kernels_bf16(int M, bool gated, bool exact, StreamKernel *out);
+int stream_kernels_row(int M, bool gated, bool exact, StreamKernel *out);
+int stream_kernels_block(int M, bool gated, bool exact, StreamKernel *out);
+int tile_kernels_bf16(bool gated, bool exact, TileKernel *out);
+int tile_kernels_row(bool gated, bool exact, TileKernel *out);
+int tile_kernels_block(bool gated, bool exact, TileKernel *out);
 
 }  // namespace skg_host

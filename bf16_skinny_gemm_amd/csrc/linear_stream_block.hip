@@ -1,0 +1,11 @@
+// The streaming projection kernels on e4m3 with block scales.
+#include "linear_stream.hpp"
+
+namespace skg_host {
+
+int stream_kernels_block(int M, bool gated, bool exact, StreamKernel *out)
+{
+    return stream_pick<2>(M, gated, exact, out);
+}
+
+}  // namespace skg_host

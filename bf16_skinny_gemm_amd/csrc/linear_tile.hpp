@@ -1,51 +1,38 @@
-// The projection kernel for many rows of x: blocks of BN x BM outputs, both operands
-// staged through LDS.
+// The projection kernel for many rows of x: blocks of outputs whose W and x are staged
+// through LDS and shared by the block's waves.
 //
-// A stage is 128 bytes of K (64 bfloat16 or 128 e4m3: one block of scales) of the
-// block's BN rows of W and BM rows of x. It is fetched by buffer loads that write LDS
-// directly, one stage ahead of the products, into the other of two buffers; the only
-// synchronisation per stage is one wait and one barrier. The loads write LDS in lane
-// order, so the layout is chosen by what each lane asks for: piece j (16 bytes) of row r
-// lies at position j ^ (r % 8) of the row's 128 bytes, and the 16-byte operand reads of
-// eight neighbouring rows then touch every bank once.
+// A stage is 128 bytes of K (64 bfloat16 or 128 e4m3: one block of scales) of the block's
+// rows of W and x, fetched by buffer loads that write LDS directly into one of two
+// buffers. The loads write LDS in lane order, so the layout is chosen by what each lane
+// asks for: piece j (16 bytes) of row r lies at position j ^ (r % 8) of the row's 128
+// bytes, and the 16-byte operand reads of eight neighbouring rows touch every bank once.
 //
 // W is the A operand (rows of D) and x the B operand (columns), so a lane holds four
-// consecutive output features of one row of y.
+// consecutive output features of one row of y. A wave multiplies TN x TM fragments; per
+// stage it reads TN + TM of them from LDS, so large wave tiles keep LDS below the matrix
+// pipe: 128 x 128 outputs read 32 KB a stage for 2048 clocks of products.
+//
+// Within a stage the wave goes along its TN fragments of W, reading the next while it
+// multiplies the current one with all TM of x. Behind the last of those reads comes the
+// stage's main barrier: the next stage is whole, and the buffer of this stage's W is
+// free. The products that are left (one and a half rows) cover the reads of the next
+// stage's x and first W fragment and the issue of later loads. x is in registers from
+// there on, so a second barrier early in a stage frees its x. With three buffers for W
+// and two for x the loads are issued two stages ahead: fetched one stage ahead, the
+// largest tile's stages took 3900 clocks for 2048 clocks of products.
+//
+// The loop over the stages has no branch (behind one, the compiler moved the sums between
+// the two register files at every step): stages past the last read zeros, since every
+// load past K does, and add nothing.
 #pragma once
 
+#include "lds_load.hpp"
 #include "linear.hpp"
 
 namespace skg {
 
-// A buffer load of 16 bytes per lane into LDS, lane i at lds + 16 i. Written as one
-// instruction block because the compiler makes every later LDS read wait for all loads
-// into LDS it knows of; it has no output register, and stage_wait() waits for it. M0
-// holds the LDS address; nothing else in these kernels uses M0 (the compiler reserves it
-// and sets it right before its own uses).
-__device__ __forceinline__ void load_to_lds(const u32x4 &rsrc, unsigned offset, unsigned lds)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds), "v"(offset), "s"(rsrc)
-                 : "memory");
-}
-
-// This wave's loads into LDS have landed.
-__device__ __forceinline__ void stage_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-__device__ __forceinline__ u32x4 rsrc_words(const void *base, unsigned bytes)
-{
-    const unsigned long long p = (unsigned long long)base;
-    u32x4 r;
-    r[0] = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)p);
-    r[1] = (unsigned)__builtin_amdgcn_readfirstlane((int)(unsigned)(p >> 32)) & 0xFFFFu;
-    r[2] = (unsigned)__builtin_amdgcn_readfirstlane((int)bytes);
-    r[3] = kBufferFlags;
-    return r;
-}
-
-// MODE and EXACT as in linear_small.hpp. WN x WM waves, each TN x TM instructions of
-// 16 x 16.
+// MODE and EXACT as in mfma_bytes. WN x WM waves, each TN x TM fragments of 16 x 16
+// (GATED: half of TN for each weight).
 template <int MODE, bool EXACT, bool GATED, int WN, int WM, int TN, int TM>
 __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int nt, int mt)
 {
@@ -54,11 +41,19 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
     constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
     constexpr int MATS = GATED ? 2 : 1;
     constexpr int NB = BN / MATS;          // output features per block
-    constexpr int TF = TN / MATS;          // instructions per wave along them
-    constexpr int STAGE = (BN + BM) * 128;
+    constexpr int TF = TN / MATS;          // fragments per wave along them
+    constexpr int WBUFS = 3, XBUFS = 2;
+    constexpr int WBUF = BN * 128, XBUF = BM * 128;
     constexpr int WL = NB / 8 / WAVES, XL = BM / 8 / WAVES;  // loads per wave and stage
-    static_assert(TN % MATS == 0 && NB % (8 * WAVES) == 0 && BM % (8 * WAVES) == 0, "whole loads per wave");
-    __shared__ uint8_t smem[2][STAGE];
+    constexpr int XS = XL + (BLOCK ? 1 + MATS : 0);          // of x and the scales
+    constexpr int LOADS = MATS * WL + XS;
+    // scales of a stage, per wave: one float for each of its rows of x and fragments of W
+    constexpr int SBUF = BLOCK ? (1 + MATS) * 256 : 0;
+    constexpr int SLOTS = TM / 2 + TM;     // products behind a stage's main barrier
+    static_assert(TN >= 4 && TN % 2 == 0 && TN % MATS == 0 && TM % 2 == 0, "fragments");
+    static_assert(NB % (8 * WAVES) == 0 && BM % (8 * WAVES) == 0, "whole loads per wave");
+    static_assert(TM <= 4 || !BLOCK, "a wave's scales of x are one load");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[WBUFS * WBUF + XBUFS * XBUF + WAVES * XBUFS * SBUF];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -86,44 +81,59 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
     for (int q = 0; q < MATS; ++q)
         wr[q] = rsrc_words(a.w[q] + (int64_t)n0 * KB, (unsigned)vn * (unsigned)KB);
     const u32x4 xr = rsrc_words(a.x + (int64_t)m0 * a.ldx, (unsigned)(vm - 1) * (unsigned)a.ldx + (unsigned)KB);
-    const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)&smem[0][0];
+    const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
     const int lrow = lane >> 3;
     const unsigned piece = (unsigned)((lane & 7) ^ lrow) * 16u;
 
-    auto issue = [&](int s) {
-        const unsigned k = (unsigned)s * 128u + piece;
-        const bool in = k < (unsigned)KB;
-        const unsigned lds = lds0 + (unsigned)(s & 1) * STAGE;
+    const int sbase = WBUFS * WBUF + XBUFS * XBUF + wave * XBUFS * SBUF;  // this wave's scales
+    u32x4 xsr, wsr[MATS];
+    if constexpr (BLOCK) {
+        xsr = rsrc_words(a.xs + (int64_t)m0 * a.kb, (unsigned)(vm * a.kb) * 4u);
 #pragma unroll
         for (int q = 0; q < MATS; ++q)
-#pragma unroll
-            for (int i = 0; i < WL; ++i) {
-                const int c = wave * WL + i;  // 8 rows each
-                load_to_lds(wr[q], in ? (unsigned)(c * 8 + lrow) * (unsigned)KB + k : kOutOfRange,
-                            lds + (unsigned)(q * NB + c * 8) * 128u);
-            }
-#pragma unroll
-        for (int i = 0; i < XL; ++i) {
-            const int c = wave * XL + i;
-            load_to_lds(xr, in ? (unsigned)(c * 8 + lrow) * (unsigned)a.ldx + k : kOutOfRange,
-                        lds + (unsigned)(BN + c * 8) * 128u);
+            wsr[q] = rsrc_words(a.ws[q] + (int64_t)(n0 / 128) * a.kb,
+                                (unsigned)((n0 % 128 + vn + 127) / 128 * a.kb) * 4u);
+    }
+    // load l of this wave's share of stage s of W, into the buffer at `buf`, and of x
+    auto issue_w = [&](int s, unsigned buf, auto lc) {
+        constexpr int l = decltype(lc)::value, q = l / WL, i = l % WL;
+        const unsigned k = (unsigned)s * 128u + piece;
+        const int c = wave * WL + i;  // 8 rows each
+        load_to_lds(wr[q], k < (unsigned)KB ? (unsigned)(c * 8 + lrow) * (unsigned)KB + k : kOutOfRange,
+                    lds0 + buf + (unsigned)(q * NB + c * 8) * 128u);
+    };
+    auto issue_x = [&](int s, int par, auto lc) {
+        constexpr int l = decltype(lc)::value;
+        if constexpr (l < XL) {
+            const unsigned k = (unsigned)s * 128u + piece;
+            const int c = wave * XL + l;
+            load_to_lds(xr, k < (unsigned)KB ? (unsigned)(c * 8 + lrow) * (unsigned)a.ldx + k : kOutOfRange,
+                        lds0 + WBUFS * WBUF + (unsigned)(par * XBUF + c * 8 * 128));
+        } else if constexpr (l == XL) {
+            const int m = wm * TM * 16 + lane;
+            load4_to_lds(xsr, lane < TM * 16 && m < vm && s < a.kb ? (unsigned)(m * a.kb + s) * 4u : kOutOfRange,
+                         lds0 + (unsigned)(sbase + par * SBUF));
+        } else {
+            constexpr int q = l - XL - 1;
+            const int n = n0 % 128 + (wn * TF + lane) * 16;  // lane: a fragment of W
+            load4_to_lds(wsr[q],
+                         lane < TF && n - n0 % 128 < vn && s < a.kb ? (unsigned)(n / 128 * a.kb + s) * 4u : kOutOfRange,
+                         lds0 + (unsigned)(sbase + par * SBUF + 256 * (1 + q)));
         }
     };
 
-    // scales of the block of K that stage s holds: x per row, W per 128 features
-    float xsc[BLOCK ? TM : 1], wsc[BLOCK ? TN : 1];
-    auto scales = [&](int s) {
+    // scales of the block of K that a stage holds, by the parity of the stage
+    float xsc[2][BLOCK ? TM : 1], wsc[2][BLOCK ? TN : 1];
+    auto read_scales = [&](auto pc) {
+        constexpr int p = decltype(pc)::value;
         if constexpr (BLOCK) {
+            const float *f = reinterpret_cast<const float *>(smem + sbase + p * SBUF);
 #pragma unroll
-            for (int j = 0; j < TM; ++j) {
-                const int m = m0 + (wm * TM + j) * 16 + i16;
-                xsc[j] = a.xs[(int64_t)(m < a.M ? m : a.M - 1) * a.kb + s];
-            }
+            for (int j = 0; j < TM; ++j)
+                xsc[p][j] = f[j * 16 + i16];
 #pragma unroll
-            for (int i = 0; i < TN; ++i) {
-                const int n = n0 + (wn * TF + i % TF) * 16;
-                wsc[i] = a.ws[i / TF][(int64_t)((n < a.N ? n : a.N - 1) / 128) * a.kb + s];
-            }
+            for (int i = 0; i < TN; ++i)
+                wsc[p][i] = f[64 * (1 + i / TF) + i % TF];
         }
     };
 
@@ -134,138 +144,152 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
         for (int j = 0; j < TM; ++j)
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // rows of this wave's fragments in a stage; piece p of row r is at p ^ (r % 8)
-    int arow[TN], brow[TM];
+    // this lane's pieces of a fragment's row; piece p of row r is at p ^ (r % 8)
+    const int p0 = (g ^ (i16 & 7)) * 16, p1 = ((g + 4) ^ (i16 & 7)) * 16;
+    const int abase = wn * TF * 16 + i16, bbase = wm * TM * 16 + i16;
+    u32x4 af[2][2], bf[2][TM][2];
+    auto read_a = [&](const uint8_t *st, int i, u32x4 (&f)[2]) {
+        const uint8_t *r = st + (abase + (i / TF) * NB + i % TF * 16) * 128;
+        f[0] = *reinterpret_cast<const u32x4 *>(r + p0);
+        f[1] = *reinterpret_cast<const u32x4 *>(r + p1);
+    };
+    auto read_b = [&](const uint8_t *st, int j, u32x4 (&f)[2]) {
+        const uint8_t *r = st + (bbase + j * 16) * 128;
+        f[0] = *reinterpret_cast<const u32x4 *>(r + p0);
+        f[1] = *reinterpret_cast<const u32x4 *>(r + p1);
+    };
+
+    // wcur, wnext: the buffers of W of stages s and s + 1; that of s + 3 is wcur again
+    auto stage = [&](int s, unsigned wcur, unsigned wnext, auto pc) {
+        constexpr int P = decltype(pc)::value;
+        const uint8_t *st = smem + wcur, *xn = smem + WBUFS * WBUF + (P ^ 1) * XBUF;
+        static_for<0, TN>([&](auto ic) {
+            constexpr int i = decltype(ic)::value;
+            if constexpr (i + 1 < TN)
+                read_a(st, i + 1, af[(i + 1) & 1]);
+            static_for<0, TM>([&](auto jc) {
+                constexpr int j = decltype(jc)::value;
+                f32x4 &c = acc[i][j];
+                if constexpr (!FP8) {
+                    c = mfma_bf16(af[i & 1][0], bf[P][j][0], c);
+                    c = mfma_bf16(af[i & 1][1], bf[P][j][1], c);
+                } else if constexpr (!BLOCK) {
+                    c = mfma_bytes<EXACT>(af[i & 1], bf[P][j], c);
+                } else {
+                    const f32x4 p = mfma_bytes<EXACT>(af[i & 1], bf[P][j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                    const float sc = xsc[P][j] * wsc[P][i];
 #pragma unroll
-    for (int i = 0; i < TN; ++i)
-        arow[i] = (i / TF) * NB + (wn * TF + i % TF) * 16 + i16;
+                    for (int e = 0; e < 4; ++e)
+                        c[e] = __builtin_fmaf(p[e], sc, c[e]);
+                }
+                if constexpr (i == 0 && j == TM - 1) {
+                    // every wave has this stage's x in registers: its buffer is free
+                    asm volatile("" ::: "memory");
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                }
+                if constexpr (i == 1)
+                    static_for<j * XS / TM, (j + 1) * XS / TM>([&](auto l) { issue_x(s + 2, P, l); });
+                if constexpr (i == TN - 2 && j == TM / 2 - 1) {
+                    // This wave has read the stage's W, and its loads of the next stage are
+                    // done: behind them are those of W and x two stages ahead.
+                    lds_read_wait();
+                    stage_wait<LOADS>();
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                }
+                if constexpr ((i == TN - 2 && j >= TM / 2) || i == TN - 1) {
+                    constexpr int q = i == TN - 1 ? TM / 2 + j : j - TM / 2;
+                    if constexpr (q < TM)
+                        read_b(xn, q, bf[P ^ 1][q]);
+                    if constexpr (q == TM) {
+                        read_a(smem + wnext, 0, af[0]);
+                        read_scales(std::integral_constant<int, P ^ 1>{});
+                    }
+                    static_for<q * (MATS * WL) / SLOTS, (q + 1) * (MATS * WL) / SLOTS>(
+                        [&](auto l) { issue_w(s + 3, wcur, l); });
+                }
+                if constexpr (!BLOCK)
+                    __builtin_amdgcn_sched_barrier(0);
+            });
+        });
+    };
+
+    // loads in the order in which the stages wait for them
+    auto all_w = [&](int s) {
+        static_for<0, MATS * WL>([&](auto l) { issue_w(s, (unsigned)(s * WBUF), l); });
+    };
+    auto all_x = [&](int s) { static_for<0, XS>([&](auto l) { issue_x(s, s, l); }); };
+    all_w(0);
+    all_x(0);
+    all_w(1);
+    all_x(1);
+    all_w(2);
+    stage_wait<LOADS + MATS * WL>();
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < TM; ++j)
-        brow[j] = BN + (wm * TM + j) * 16 + i16;
-    const int p0 = (g ^ (i16 & 7)) * 16, p1 = ((g + 4) ^ (i16 & 7)) * 16;
-
-    issue(0);
-    scales(0);
-    for (int s = 0; s < stages; ++s) {
-        stage_wait();
-        __syncthreads();  // the stage is whole, and every wave has left the other buffer
-        float xc[BLOCK ? TM : 1], wc[BLOCK ? TN : 1];
-        if constexpr (BLOCK) {
-#pragma unroll
-            for (int j = 0; j < TM; ++j)
-                xc[j] = xsc[j];
-#pragma unroll
-            for (int i = 0; i < TN; ++i)
-                wc[i] = wsc[i];
-        }
-        if (s + 1 < stages) {
-            issue(s + 1);
-            scales(s + 1);
-        }
-        const uint8_t *st = smem[s & 1];
-        if constexpr (!FP8) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4 af[TN], bf[TM];
-#pragma unroll
-                for (int i = 0; i < TN; ++i)
-                    af[i] = *reinterpret_cast<const u32x4 *>(st + arow[i] * 128 + (h ? p1 : p0));
-#pragma unroll
-                for (int j = 0; j < TM; ++j)
-                    bf[j] = *reinterpret_cast<const u32x4 *>(st + brow[j] * 128 + (h ? p1 : p0));
-#pragma unroll
-                for (int i = 0; i < TN; ++i)
-#pragma unroll
-                    for (int j = 0; j < TM; ++j)
-                        acc[i][j] = mfma_bf16(af[i], bf[j], acc[i][j]);
-            }
-        } else {
-            u32x4 bf[TM][2];
-#pragma unroll
-            for (int j = 0; j < TM; ++j) {
-                bf[j][0] = *reinterpret_cast<const u32x4 *>(st + brow[j] * 128 + p0);
-                bf[j][1] = *reinterpret_cast<const u32x4 *>(st + brow[j] * 128 + p1);
-            }
-#pragma unroll
-            for (int i = 0; i < TN; ++i) {
-                const u32x4 af[2] = {*reinterpret_cast<const u32x4 *>(st + arow[i] * 128 + p0),
-                                     *reinterpret_cast<const u32x4 *>(st + arow[i] * 128 + p1)};
-#pragma unroll
-                for (int j = 0; j < TM; ++j) {
-                    if constexpr (BLOCK) {
-                        const f32x4 p = mfma_bytes<EXACT>(af, bf[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-                        const float sc = xc[j] * wc[i];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[i][j][e] = __builtin_fmaf(p[e], sc, acc[i][j][e]);
-                    } else {
-                        acc[i][j] = mfma_bytes<EXACT>(af, bf[j], acc[i][j]);
-                    }
-                }
-            }
-        }
+        read_b(smem + WBUFS * WBUF, j, bf[0][j]);
+    read_a(smem, 0, af[0]);
+    read_scales(std::integral_constant<int, 0>{});
+    unsigned w0 = 0, w1 = WBUF, w2 = 2 * WBUF;
+    for (int s = 0; s < stages; s += 2) {
+        stage(s, w0, w1, std::integral_constant<int, 0>{});
+        stage(s + 1, w1, w2, std::integral_constant<int, 1>{});
+        const unsigned w = w0;
+        w0 = w2;
+        w2 = w1;
+        w1 = w;
     }
 
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
+    static_for<0, TM>([&](auto jc) {
+        constexpr int j = decltype(jc)::value;
         const int m = m0 + (wm * TM + j) * 16 + i16;
-        if (m >= a.M)
-            continue;
-        const float xs = MODE == 1 ? a.xs[m] : 1.0f;
-#pragma unroll
-        for (int i = 0; i < TF; ++i) {
-            const int n = n0 + (wn * TF + i) * 16 + g * 4;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (n + e >= a.N)
-                    continue;
-                float z = acc[i][j][e], u = GATED ? acc[TF * (MATS - 1) + i][j][e] : 0.0f;
-                if constexpr (MODE == 1) {
-                    z *= xs * a.ws[0][n + e];
-                    if constexpr (GATED)
-                        u *= xs * a.ws[1][n + e];
-                }
-                put(a, finish<GATED>(a, z, u, m, n + e), m, n + e);
-            }
-        }
-    }
+        if (m < a.M)
+            static_for<0, TF>([&](auto ic) {
+                constexpr int i = decltype(ic)::value;
+                finish4<MODE, GATED>(a, acc[i][j], acc[TF * (MATS - 1) + i][j], m, n0 + (wn * TF + i) * 16 + g * 4);
+            });
+    });
 }
 
 }  // namespace skg
 
 namespace skg_host {
 
-struct TileKernel {
-    const void *fn;
-    int bn, bm, threads;  // outputs per block along N and M
-};
-
-// size 0: the smallest tile, 2: the largest
-template <int MODE, bool EXACT, bool GATED>
-TileKernel tile_of(int size)
+template <int MODE, bool EXACT, bool GATED, int WN, int WM, int TN, int TM>
+TileKernel tile_of(float stage_us)
 {
-    using namespace skg;
-    constexpr int G = GATED ? 2 : 1;
-    if (size == 0)
-        return {reinterpret_cast<const void *>(&linear_tile_kernel<MODE, EXACT, GATED, 2, 2, 2, 2>), 64 / G, 64, 256};
-    if (size == 1)
-        return {reinterpret_cast<const void *>(&linear_tile_kernel<MODE, EXACT, GATED, 2, 2, 4, 4>), 128 / G, 128, 256};
-    return {reinterpret_cast<const void *>(&linear_tile_kernel<MODE, EXACT, GATED, 4, 2, 4, 8>), 256 / G, 256, 512};
+    return TileKernel{reinterpret_cast<const void *>(&skg::linear_tile_kernel<MODE, EXACT, GATED, WN, WM, TN, TM>),
+                      WN * TN * 16 / (GATED ? 2 : 1), WM * TM * 16, WN * WM, stage_us};
+}
+
+// The stage times are measured ones, full chip, each compute unit's blocks one after
+// another (two 128 x 128 blocks run beside each other on one).
+template <int MODE, bool EXACT, bool GATED>
+int tile_set(TileKernel *out)
+{
+    int n = 0;
+    if constexpr (EXACT) {  // for float32 outputs only: one tile serves them
+        out[n++] = tile_of<MODE, EXACT, GATED, 2, 2, 4, 4>(1.0f);
+    } else if constexpr (MODE == 2) {
+        out[n++] = tile_of<MODE, EXACT, GATED, 2, 2, 4, 4>(0.95f);
+        out[n++] = tile_of<MODE, EXACT, GATED, 4, 2, 4, 4>(GATED ? 1.5f : 1.25f);
+    } else {
+        out[n++] = tile_of<MODE, EXACT, GATED, 2, 2, 4, 4>(0.53f);
+        out[n++] = tile_of<MODE, EXACT, GATED, 4, 2, 4, 4>(MODE ? 0.95f : 0.84f);
+        out[n++] = tile_of<MODE, EXACT, GATED, 2, 4, 8, 4>(MODE ? 2.0f : 1.65f);
+    }
+    return n;
 }
 
 template <int MODE>
-TileKernel tile_pick(bool gated, bool exact, int size)
+int tile_pick(bool gated, bool exact, TileKernel *out)
 {
     if constexpr (MODE != 0)
-        if (exact) {  // rare and slower: the two smaller tiles serve it
-            size = size > 1 ? 1 : size;
-            return gated ? tile_of<MODE, true, true>(size) : tile_of<MODE, true, false>(size);
-        }
-    return gated ? tile_of<MODE, false, true>(size) : tile_of<MODE, false, false>(size);
+        if (exact)
+            return gated ? tile_set<MODE, true, true>(out) : tile_set<MODE, true, false>(out);
+    return gated ? tile_set<MODE, false, true>(out) : tile_set<MODE, false, false>(out);
 }
-
-TileKernel tile_kernel_bf16(bool gated, bool exact, int size);
-TileKernel tile_kernel_row(bool gated, bool exact, int size);
-TileKernel tile_kernel_block(bool gated, bool exact, int size);
 
 }  // namespace skg_host

@@ -1,11 +1,8 @@
-// The many-row projection kernels of one element type and scale mode.
+// The tiled projection kernels on bfloat16.
 #include "linear_tile.hpp"
 
 namespace skg_host {
 
-TileKernel tile_kernel_bf16(bool gated, bool exact, int size)
-{
-    return tile_pick<0>(gated, exact, size);
-}
+int tile_kernels_bf16(bool gated, bool exact, TileKernel *out) { return tile_pick<0>(gated, exact, out); }
 
 }  // namespace skg_host

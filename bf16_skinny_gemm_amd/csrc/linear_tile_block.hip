@@ -1,11 +1,8 @@
-// The many-row projection kernels of one element type and scale mode.
+// The tiled projection kernels on e4m3 with block scales.
 #include "linear_tile.hpp"
 
 namespace skg_host {
 
-TileKernel tile_kernel_block(bool gated, bool exact, int size)
-{
-    return tile_pick<2>(gated, exact, size);
-}
+int tile_kernels_block(bool gated, bool exact, TileKernel *out) { return tile_pick<2>(gated, exact, out); }
 
 }  // namespace skg_host

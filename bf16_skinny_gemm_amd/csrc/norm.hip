@@ -17,13 +17,10 @@
 #include <cstring>
 #include <mutex>
 
-#include "kernels.hpp"
+#include "ops_device.hpp"
 #include "validate_ops.hpp"
 
 namespace skg {
-
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kE4m3Max = 448.0f;
 constexpr float kLeastAmax = 0x1p-100f;  // keeps 448 / amax finite for a row of zeros
@@ -39,16 +36,6 @@ struct NormArgs {
 };
 
 enum { kOutBf16 = 0, kOutRow = 1, kOutGroup = 2 };
-
-__device__ __forceinline__ float lo_f32(unsigned p) { return __builtin_bit_cast(float, p << 16); }
-__device__ __forceinline__ float hi_f32(unsigned p) { return __builtin_bit_cast(float, p & 0xFFFF0000u); }
-
-// Two floats to packed bfloat16, nearest-even (v_cvt_pk_bf16_f32).
-__device__ __forceinline__ unsigned pack_bf16(float a, float b)
-{
-    const f32x2 v = {a, b};
-    return __builtin_bit_cast(unsigned, __builtin_convertvector(v, bf16x2_t));
-}
 
 template <int CTRL>
 __device__ __forceinline__ unsigned dpp_umax(unsigned v)
