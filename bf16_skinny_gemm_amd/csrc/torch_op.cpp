@@ -14,8 +14,10 @@
 // The operators of include/skinny_ops.h (norms, projections with an epilogue) are
 // registered below in the same way.
 #include <ATen/core/Tensor.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/library.h>
 
@@ -70,7 +72,7 @@ at::Tensor linear_cpu(const at::Tensor &x, const at::Tensor &weight)
 // The rows of a [..., width] tensor as one [M][width] matrix with a row stride: 2-D
 // tensors with unit column stride are taken as they are, others made contiguous.
 struct Rows {
-    at::Tensor t;  // keeps a copy alive until the launch
+    at::Tensor t;  // holds a copy, if one was made, until the launch
     const void *p;
     int64_t M, ld;
 };
@@ -78,13 +80,33 @@ struct Rows {
 Rows rows_of(const at::Tensor &t, int64_t width)
 {
     if (t.dim() == 2 && (t.stride(1) == 1 || width == 1) && (t.stride(0) >= width || t.size(0) == 1))
-        return Rows{t, t.data_ptr(), t.size(0), t.size(0) == 1 ? width : t.stride(0)};
+        return Rows{at::Tensor(), t.data_ptr(), t.size(0), t.size(0) == 1 ? width : t.stride(0)};
     int64_t M = 1;
     for (int64_t d = 0; d + 1 < t.dim(); ++d)
         M *= t.size(d);
+    if (t.is_contiguous())
+        return Rows{at::Tensor(), t.data_ptr(), M, width};
     at::Tensor c = t.contiguous();
-    return Rows{c, c.data_ptr(), M, width};
+    const void *p = c.data_ptr();
+    return Rows{std::move(c), p, M, width};
 }
+
+// An output tensor straight from the caching allocator: the dispatcher's round for it
+// took 0.4 us of an eager call's 5.4.
+at::Tensor output(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &x)
+{
+    return at::Tensor(at::detail::empty_cuda(shape, type, x.device(), std::nullopt));
+}
+
+// Makes x's device current for the call where it is not.
+struct OnDevice {
+    std::optional<c10::DeviceGuard> guard;
+    explicit OnDevice(const at::Tensor &x)
+    {
+        if (x.device().index() != c10::hip::current_device())
+            guard.emplace(x.device());
+    }
+};
 
 void check_gpu(const char *op, const at::Tensor &x, const at::Tensor &t, const char *name, at::ScalarType type)
 {
@@ -110,9 +132,9 @@ void check_status(const char *op, int st)
     TORCH_CHECK(st == SKINNY_OK, op, ": ", skinny_gemm_status_string(st));
 }
 
-std::vector<int64_t> with_last(const at::Tensor &x, int64_t last)
+c10::SmallVector<int64_t, 6> with_last(const at::Tensor &x, int64_t last)
 {
-    std::vector<int64_t> shape(x.sizes().begin(), x.sizes().end());
+    c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
     shape.back() = last;
     return shape;
 }
@@ -134,18 +156,18 @@ std::tuple<at::Tensor, at::Tensor, at::Tensor> norm_gpu(const char *op, const at
         TORCH_CHECK_VALUE(residual->sizes() == x.sizes(), op, ": residual must have x's shape ", x.sizes(), ", got ",
                           residual->sizes());
     }
-    c10::DeviceGuard guard(x.device());
+    const OnDevice on(x);
     const Rows xr = rows_of(x, D);
     Rows rr{};
     at::Tensor h, scale;
     const bool fp8 = group >= 0;
-    at::Tensor y = at::empty(x.sizes(), fp8 ? x.options().dtype(at::kFloat8_e4m3fn) : x.options());
+    at::Tensor y = output(x.sizes(), fp8 ? at::kFloat8_e4m3fn : at::kBFloat16, x);
     skinny_norm_t n{};
     n.x = xr.p;
     n.ldx = xr.ld;
     if (residual) {
         rr = rows_of(*residual, D);
-        h = at::empty(x.sizes(), x.options());
+        h = output(x.sizes(), at::kBFloat16, x);
         n.residual = rr.p;
         n.ldr = rr.ld;
         n.residual_out = h.data_ptr();
@@ -158,10 +180,10 @@ std::tuple<at::Tensor, at::Tensor, at::Tensor> norm_gpu(const char *op, const at
     n.D = size32(op, D, "the width");
     n.eps = (float)eps;
     if (fp8) {
-        std::vector<int64_t> shape(x.sizes().begin(), x.sizes().end() - 1);
+        c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end() - 1);
         if (group)
             shape.push_back((D + group - 1) / group);
-        scale = at::empty(shape, x.options().dtype(at::kFloat));
+        scale = output(shape, at::kFloat, x);
         n.scale = scale.data_ptr<float>();
         n.group = (int32_t)group;
     }
@@ -250,7 +272,7 @@ at::Tensor linear_any(const char *op, const at::Tensor &x, const at::Tensor *xs,
     const at::Tensor &w0 = sides[0].w;
     TORCH_CHECK_VALUE(w0.dim() == 2, op, ": the weight must be [N, K], got ", w0.sizes());
     const int64_t N = w0.size(0);
-    c10::DeviceGuard guard(x.device());
+    const OnDevice on(x);
     const Rows xr = rows_of(x, K);
     skinny_linear_t a{};
     a.M = size32(op, xr.M, "the number of rows");
@@ -281,7 +303,7 @@ at::Tensor linear_any(const char *op, const at::Tensor &x, const at::Tensor *xs,
     }
     TORCH_CHECK_VALUE(mats == 1 || (N > 0 && K > 0) || xr.M == 0, op, ": the gated form needs N and K above 0");
     Rows rr{};
-    const std::vector<int64_t> shape = with_last(x, N);
+    const auto shape = with_last(x, N);
     if (residual) {
         check_gpu(op, x, *residual, "residual", at::kBFloat16);
         TORCH_CHECK_VALUE(residual->sizes() == at::IntArrayRef(shape), op, ": residual must be ", at::IntArrayRef(shape),
@@ -290,7 +312,7 @@ at::Tensor linear_any(const char *op, const at::Tensor &x, const at::Tensor *xs,
         a.residual = rr.p;
         a.ldr = rr.ld;
     }
-    at::Tensor y = at::empty(shape, x.options().dtype(out_f32 ? at::kFloat : at::kBFloat16));
+    at::Tensor y = output(shape, out_f32 ? at::kFloat : at::kBFloat16, x);
     a.y = y.data_ptr();
     a.ldy = N;
     a.out_f32 = out_f32;
