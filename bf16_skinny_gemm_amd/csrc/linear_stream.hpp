@@ -175,6 +175,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
         const int m = m0 + j * 16 + (l & 15), n = n0 + i * 16 + (l >> 4) * 4;
         if (m >= a.M || n >= a.N)
             continue;
+        const u32x2 r = residual4(a, m, n);
         f32x4 z = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, u = z;
 #pragma unroll
         for (int k = 0; k < WAVES; ++k) {
@@ -182,7 +183,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
             if constexpr (GATED)
                 u += HALF ? part[(k * TM + j) * 64 + 32 + l] : part[((k * TN + TF + i) * TM + j) * 64 + l];
         }
-        finish4<MODE, GATED>(a, z, u, m, n);
+        finish4<MODE, GATED>(a, z, u, r, m, n);
     }
 }
 

@@ -61,12 +61,12 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
     const int wn = wave % WN, wm = wave / WN;
 
     // Workgroups go to the 8 XCDs in turn. Each XCD takes a contiguous run of tiles, in
-    // groups of 8 rows of tiles by column, so that its L2 serves one group's W and x.
+    // groups of 4 or 8 rows of tiles by column, so that its L2 serves one group's W and x.
     const int total = nt * mt;
     const int q8 = total / 8, r8 = total % 8;
     const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
     const int t = xcd * q8 + (xcd < r8 ? xcd : r8) + at;
-    constexpr int GROUP = 8;
+    constexpr int GROUP = BN * BM >= 65536 ? 4 : 8;  // 4096^3: 121 us against 128 with 8
     const int per = GROUP * nt;
     const int first = t / per * GROUP;
     const int rows = mt - first < GROUP ? mt - first : GROUP;
@@ -167,11 +167,16 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
             constexpr int i = decltype(ic)::value;
             if constexpr (i + 1 < TN)
                 read_a(st, i + 1, af[(i + 1) & 1]);
+            // the two products of a sum stay TM apart: back to back, the second would wait
+            if constexpr (!FP8)
+                static_for<0, TM>([&](auto jc) {
+                    constexpr int j = decltype(jc)::value;
+                    acc[i][j] = mfma_bf16(af[i & 1][0], bf[P][j][0], acc[i][j]);
+                });
             static_for<0, TM>([&](auto jc) {
                 constexpr int j = decltype(jc)::value;
                 f32x4 &c = acc[i][j];
                 if constexpr (!FP8) {
-                    c = mfma_bf16(af[i & 1][0], bf[P][j][0], c);
                     c = mfma_bf16(af[i & 1][1], bf[P][j][1], c);
                 } else if constexpr (!BLOCK) {
                     c = mfma_bytes<EXACT>(af[i & 1], bf[P][j], c);
@@ -242,14 +247,50 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
         w1 = w;
     }
 
-    static_for<0, TM>([&](auto jc) {
-        constexpr int j = decltype(jc)::value;
-        const int m = m0 + (wm * TM + j) * 16 + i16;
-        if (m < a.M)
-            static_for<0, TF>([&](auto ic) {
+    // The sums go through LDS, so that a wave stores whole rows of the tile: straight from
+    // the registers a store instruction covers 32 bytes of each of 16 rows, and the tile
+    // of 256 x 256 spent 30 us of 4096^3's 128 outside its stages. Piece p (4 outputs) of row
+    // r lies at position p ^ (r % 16), so neither side meets on a bank.
+    constexpr int SMEM = WBUFS * WBUF + XBUFS * XBUF + WAVES * XBUFS * SBUF;
+    constexpr int PASSES = BN * BM * 4 > SMEM ? 2 : 1;
+    constexpr int JP = TM / PASSES, RP = WM * JP * 16;  // fragments per wave, rows per pass
+    constexpr int PL = NB / 4;                          // lanes per row
+    constexpr int RI = 64 / PL, ITERS = RP / (RI * WAVES), BATCH = ITERS < 4 ? ITERS : 4;
+    static_assert(PL <= 64 && RP % (RI * WAVES) == 0 && ITERS % BATCH == 0, "rows per wave");
+    const int pl = lane % PL, sub = lane / PL, n = n0 + pl * 4;
+    stage_wait();  // the loads past the last stage have written their zeros
+    static_for<0, PASSES>([&](auto qc) {
+        constexpr int q = decltype(qc)::value;
+        __syncthreads();
+        static_for<0, JP>([&](auto jc) {
+            constexpr int j = decltype(jc)::value;
+            const int row = (wm * JP + j) * 16 + i16;
+            static_for<0, TN>([&](auto ic) {
                 constexpr int i = decltype(ic)::value;
-                finish4<MODE, GATED>(a, acc[i][j], acc[TF * (MATS - 1) + i][j], m, n0 + (wn * TF + i) * 16 + g * 4);
+                const int p = ((i / TF) * NB + (wn * TF + i % TF) * 16) / 4 + g;
+                *reinterpret_cast<f32x4 *>(smem + row * (BN * 4) + (p ^ i16) * 16) = acc[i][q * JP + j];
             });
+        });
+        __syncthreads();
+        for (int b = 0; b < ITERS; b += BATCH) {
+            int m[BATCH];
+            u32x2 res[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int row = ((b + k) * WAVES + wave) * RI + sub;
+                m[k] = m0 + (row / (JP * 16) * TM + q * JP) * 16 + row % (JP * 16);
+                res[k] = m[k] < a.M ? residual4(a, m[k], n) : u32x2{0, 0};
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int row = ((b + k) * WAVES + wave) * RI + sub;
+                const uint8_t *at_row = smem + row * (BN * 4);
+                const f32x4 z = *reinterpret_cast<const f32x4 *>(at_row + (pl ^ (row & 15)) * 16);
+                const f32x4 u = GATED ? *reinterpret_cast<const f32x4 *>(at_row + ((PL + pl) ^ (row & 15)) * 16) : z;
+                if (m[k] < a.M && n < a.N)
+                    finish4<MODE, GATED>(a, z, u, res[k], m[k], n);
+            }
+        }
     });
 }
 
