@@ -98,19 +98,20 @@ struct Choice {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The kernel whose estimated time is least. The estimate of a streaming kernel has three
-// parts: the bytes of W and x once from HBM; the bytes that the fullest compute unit takes
-// into LDS; and the round trips its waves wait for one after another (a ring of two stages
-// hides a part of them). A part of all three is paid beside the largest, since they
-// overlap incompletely. That of a tiled kernel is its measured time per stage. The
-// constants were fitted to the times of 117 kernels at 583 sizes of each type (K 512 to
-// 8192, N 256 to 12576, M 1 to 4096): the choice takes 2.7% longer than the best of all
-// kernels on average, half of them within 0.5%.
+// The kernel whose estimated time, in microseconds, is least. The estimate of a streaming
+// kernel has three parts: W and x once from memory; the bytes that the fullest compute
+// unit takes into LDS, at 97.5 KB/us; and the round trips of 0.93 us that its waves wait
+// for one after another (a ring of two stages hides a part of them). A part of all three
+// is paid beside the largest, since they overlap incompletely, and each turn of blocks
+// adds its start and the sum of its waves. That of a tiled kernel is its time per stage.
+// The constants were fitted to the times of 67 kernels at 932 sizes of each type (K 512
+// to 8192, N 256 to 12576, M 1 to 4096): the choice takes 2.2% longer than the best of
+// all kernels on average and 8% at the 90th percentile.
 Choice choose(int mode, bool gated, bool exact, int M, int N, int64_t kbytes, int cus)
 {
     const int mats = gated ? 2 : 1;
     const double stages = (double)ceil_div(kbytes, 128);
-    const double hbm = ((double)mats * N + M) * (double)kbytes / 3.07e6;
+    const double hbm = ((double)mats * N + M) * (double)kbytes / 22.5e6;
     Choice best{};
     double least = 0.0;
     auto offer = [&](const Choice &c, double us) {
@@ -131,11 +132,11 @@ Choice choose(int mode, bool gated, bool exact, int M, int N, int64_t kbytes, in
         const double turns = std::ceil((double)(c.nt * c.mt) / (cus * at_once));
         if (at_once > per_cu)
             at_once = per_cu;
-        const double lds = per_cu * stages * k.stage / 86700.0;
-        const double trips = 0.276 * std::ceil(stages * per_cu / (k.waves * at_once * (1.0 + 1.2 * (k.ring - 1))));
+        const double lds = per_cu * stages * k.stage / 97500.0;
+        const double trips = 0.932 * std::ceil(stages * per_cu / (k.waves * at_once * (1.0 + 1.1 * (k.ring - 1))));
         double most = hbm > lds ? hbm : lds;
         most = most > trips ? most : trips;
-        offer(c, 2.8 + most + 0.185 * (hbm + lds + trips) + turns * (1.0 + 0.025 * k.waves * k.tiles));
+        offer(c, 3.0 + most + 0.2 * (hbm + lds + trips) + turns * (0.344 + 0.0292 * k.waves * k.tiles));
     }
     if (M <= 16)  // W once: a tile of many rows only adds work
         return best;
@@ -146,7 +147,8 @@ Choice choose(int mode, bool gated, bool exact, int M, int N, int64_t kbytes, in
     for (int i = 0; i < ntk; ++i) {
         const TileKernel &k = t[i];
         const Choice c{k.fn, ceil_div(N, k.nb), ceil_div(M, k.bm), k.waves};
-        offer(c, 9.4 + stages * k.stage_us * (double)ceil_div(c.nt * c.mt, cus));
+        const double per_cu = (double)ceil_div(c.nt * c.mt, cus);
+        offer(c, 8.2 + per_cu * (0.5 + stages * k.stage_us));
     }
     return best;
 }

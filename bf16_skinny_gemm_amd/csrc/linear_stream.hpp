@@ -211,23 +211,27 @@ int stream_set(int M, StreamKernel *out)
     int n = 0;
     if (M <= 8) {
         out[n++] = stream_of<MODE, E, GATED, 8, 1, 8, 2, 8, true>();
+        out[n++] = stream_of<MODE, E, GATED, 8, 1, 8, 3, 8, true>();
         out[n++] = stream_of<MODE, E, GATED, 16, 1, 8, 2, 4, true>();
         out[n++] = stream_of<MODE, E, GATED, 16, 1, 8, 2, 8, true>();
-        out[n++] = stream_of<MODE, E, GATED, 32, 1, 8, 2, 4, true>();
     } else if (M <= 16) {
         out[n++] = stream_of<MODE, E, GATED, 8, 1, 16, 2, 8, true>();
         out[n++] = stream_of<MODE, E, GATED, 16, 1, 16, 2, 4, true>();
         out[n++] = stream_of<MODE, E, GATED, 16, 1, 16, 2, 8, true>();
         out[n++] = stream_of<MODE, E, GATED, 32, 1, 16, 2, 4, true>();
     } else {
-        out[n++] = stream_of<MODE, EXACT, GATED, 8, 1, 16, 2, 8, false>();
         out[n++] = stream_of<MODE, EXACT, GATED, 16, 1, 16, 1, 8, false>();
         out[n++] = stream_of<MODE, EXACT, GATED, 16, 2, 32, 2, 4, false>();
         out[n++] = stream_of<MODE, EXACT, GATED, 32, 2, 32, 1, 4, false>();
+        out[n++] = stream_of<MODE, EXACT, GATED, 32, 2, 32, 2, 4, false>();
         out[n++] = stream_of<MODE, EXACT, GATED, 32, 4, 64, 1, 4, false>();
-        if constexpr (!GATED)
+        out[n++] = stream_of<MODE, EXACT, GATED, 32, 4, 64, 1, 8, false>();
+        if constexpr (!GATED) {
+            out[n++] = stream_of<MODE, EXACT, GATED, 64, 3, 48, 1, 4, false>();
             out[n++] = stream_of<MODE, EXACT, GATED, 64, 4, 64, 1, 4, false>();
+        }
     }
+    static_assert(kStreamMost >= 8, "the largest set");
     return n;
 }
 

@@ -95,9 +95,51 @@ __device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d
     return (unsigned)v;
 }
 
-// WPR waves per row, P 16-byte pieces per lane: covers D <= WPR * 64 * 8 * P, D % 8 == 0.
-// Piece p of a lane is p * WPR * 64 + lane, so a wave reads 1 KiB at a time and 16
-// neighbouring lanes hold 128 consecutive columns: a scale group is a 16-lane row.
+// Vectors in memory at any alignment: global memory takes unaligned 16-byte accesses, so
+// rows of odd width or stride move in the same instructions as aligned ones.
+typedef u32x4 __attribute__((aligned(1))) u32x4_any;
+typedef u32x2 __attribute__((aligned(1))) u32x2_any;
+
+// Eight bfloat16 values from p, of which `left` (> 0) exist: the others are 0.
+__device__ __forceinline__ u32x4 load8(const uint16_t *p, int left)
+{
+    if (left >= 8)
+        return *reinterpret_cast<const u32x4_any *>(p);
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < left)
+            v[e >> 1] |= (unsigned)p[e] << (16 * (e & 1));
+    return v;
+}
+
+__device__ __forceinline__ void store8(uint16_t *p, const u32x4 &v, int left)
+{
+    if (left >= 8) {
+        *reinterpret_cast<u32x4_any *>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < left)
+            p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+}
+
+__device__ __forceinline__ void store8(uint8_t *p, const u32x2 &v, int left)
+{
+    if (left >= 8) {
+        *reinterpret_cast<u32x2_any *>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < left)
+            p[e] = (uint8_t)(v[e >> 2] >> (8 * (e & 3)));
+}
+
+// WPR waves per row, P pieces of 8 columns per lane: covers D <= WPR * 64 * 8 * P. Piece p
+// of a lane is p * WPR * 64 + lane, so a wave reads 1 KiB at a time and 16 neighbouring
+// lanes hold 128 consecutive columns: a scale group is a 16-lane row.
 template <int WPR, int P, bool RES, int OUT>
 __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArgs a)
 {
@@ -107,7 +149,6 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
     const int lane = threadIdx.x & 63;
     const int sub = wave / WPR;
     const int t = (wave % WPR) * 64 + lane;
-    const int pieces = a.D >> 3;
     __shared__ float s_sum[WPR > 1 ? ROWS * WPR : 1];
     __shared__ unsigned s_max[WPR > 1 ? ROWS * WPR : 1];
     // 64-bit rows: M * ld passes 32 bits in a long prompt
@@ -118,16 +159,16 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
     u32x4 xv[P], rv[RES ? P : 1], wv[P];
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        const int i = p * LANES + t;
-        const bool in = live && i < pieces;
-        xv[p] = in ? *reinterpret_cast<const u32x4 *>(a.x + rr * a.ldx + i * 8) : u32x4{0, 0, 0, 0};
+        const int c = (p * LANES + t) * 8;
+        const bool in = live && c < a.D;
+        xv[p] = in ? load8(a.x + rr * a.ldx + c, a.D - c) : u32x4{0, 0, 0, 0};
         if constexpr (RES)
-            rv[p] = in ? *reinterpret_cast<const u32x4 *>(a.r + rr * a.ldr + i * 8) : u32x4{0, 0, 0, 0};
+            rv[p] = in ? load8(a.r + rr * a.ldr + c, a.D - c) : u32x4{0, 0, 0, 0};
     }
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-        const int i = p * LANES + t;
-        wv[p] = live && i < pieces ? *reinterpret_cast<const u32x4 *>(a.w + i * 8) : u32x4{0, 0, 0, 0};
+        const int c = (p * LANES + t) * 8;
+        wv[p] = live && c < a.D ? load8(a.w + c, a.D - c) : u32x4{0, 0, 0, 0};
     }
 
     float hw[P][8];
@@ -156,11 +197,11 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
             }
         }
         if constexpr (RES) {
-            const int i = p * LANES + t;
+            const int c = (p * LANES + t) * 8;
             // residual_out may be residual or x: every lane has read this row's pieces it
             // overwrites, and no other lane reads them
-            if (live && i < pieces)
-                *reinterpret_cast<u32x4 *>(a.ro + rr * a.ldro + i * 8) = ho;
+            if (live && c < a.D)
+                store8(a.ro + rr * a.ldro + c, ho, a.D - c);
         }
     }
     sum = wave_sum(sum);
@@ -195,13 +236,13 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
         uint16_t *y = static_cast<uint16_t *>(a.y) + rr * a.ldy;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int i = p * LANES + t;
+            const int c = (p * LANES + t) * 8;
             u32x4 o;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 o[q] = pack_bf16(hw[p][2 * q] * f, hw[p][2 * q + 1] * f);
-            if (i < pieces)
-                *reinterpret_cast<u32x4 *>(y + i * 8) = o;
+            if (c < a.D)
+                store8(y + c, o, a.D - c);
         }
     } else {
         uint8_t *y = static_cast<uint8_t *>(a.y) + rr * a.ldy;
@@ -214,23 +255,23 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
         }
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            const int i = p * LANES + t;
+            const int c = (p * LANES + t) * 8;
             if constexpr (OUT == kOutGroup) {
                 sc = scale_of(__builtin_bit_cast(float, umax16(top[p])) * f);
                 g = f / sc;
-                if ((lane & 15) == 0 && i < pieces)
-                    a.scale[rr * a.groups + (i >> 4)] = sc;
+                if ((lane & 15) == 0 && c < a.D)
+                    a.scale[rr * a.groups + (c >> 7)] = sc;
             }
             u32x2 o;
             o[0] = pack_e4m3(hw[p][0] * g, hw[p][1] * g, hw[p][2] * g, hw[p][3] * g);
             o[1] = pack_e4m3(hw[p][4] * g, hw[p][5] * g, hw[p][6] * g, hw[p][7] * g);
-            if (i < pieces)
-                *reinterpret_cast<u32x2 *>(y + i * 8) = o;
+            if (c < a.D)
+                store8(y + c, o, a.D - c);
         }
     }
 }
 
-// Element-wise form: any D, alignment and strides; one block of 256 threads per row.
+// Rows wider than the registers of a block: one block of 256 threads per row.
 // Every value is recomputed from x and residual in each pass, and all stores come in
 // the last one, by the thread that alone reads those elements, so the accepted
 // overlaps hold here too.
@@ -374,7 +415,7 @@ int run_norm(const skinny_norm_t *n, bool fp8, hipStream_t stream)
     void *args[] = {&a};
     const bool res = n->residual != nullptr;
     const int out = !fp8 ? skg::kOutBf16 : n->group ? skg::kOutGroup : skg::kOutRow;
-    if (!norm_vector_ok(*n, fp8))
+    if (n->D > 32768)
         return ops_launch(norm_any_fn(res, out), row_grid(n->M), 256, args, stream);
     const void *fn;
     int wpr;

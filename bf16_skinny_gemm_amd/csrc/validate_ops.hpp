@@ -107,15 +107,6 @@ inline int validate_norm(const skinny_norm_t *a, bool fp8)
     return SKINNY_OK;
 }
 
-// Every row can be read and written in 16-byte pieces of x (8- or 16-byte pieces of y).
-inline bool norm_vector_ok(const skinny_norm_t &a, bool fp8)
-{
-    const bool res = a.residual != nullptr;
-    return aligned(a.x, 16) && aligned(a.weight, 16) && aligned(a.y, fp8 ? 8 : 16) && a.D % 8 == 0 &&
-           a.ldx % 8 == 0 && a.ldy % 8 == 0 && a.D <= 32768 &&
-           (!res || (aligned(a.residual, 16) && aligned(a.residual_out, 16) && a.ldr % 8 == 0 && a.ldro % 8 == 0));
-}
-
 inline int validate_linear(const skinny_linear_t *a, bool fp8)
 {
     if (!a || a->M < 0 || a->N < 0 || a->K < 0)

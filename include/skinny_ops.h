@@ -43,8 +43,7 @@ extern "C" {
  * or x itself (same pointer and stride), as may y be x in the bfloat16 form when
  * residual_out is not x; no other overlap of an output with an input or another
  * output is accepted. eps >= 0. Everything 2-byte aligned; any D and strides.
- * Fast path: pointers 16-byte aligned, D and strides multiples of 8, D <= 32768;
- * anything else runs an element-wise kernel.
+ * Rows of up to 32768 columns stay in registers; wider ones are read twice.
  */
 typedef struct skinny_norm {
     const void *x;            /* [M][D] bfloat16, row stride ldx >= D */
