@@ -596,6 +596,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     and residual_out may be given; residual_out may be residual or x, and out may be x."""
     ldx = _matrix(x, "x", torch.bfloat16, None)
     M, D = x.shape
+    if D == 0:
+        raise ValueError("the width must be above 0")
     if quant not in (None, "row", "group"):
         raise ValueError(f"quant must be None, 'row' or 'group', got {quant!r}")
     if residual is None and residual_out is not None:

@@ -148,6 +148,7 @@ std::tuple<at::Tensor, at::Tensor, at::Tensor> norm_gpu(const char *op, const at
     check_matrix(op, x, at::kBFloat16);
     check_gpu(op, x, weight, "weight", at::kBFloat16);
     const int64_t D = x.size(-1);
+    TORCH_CHECK_VALUE(D > 0, op, ": the width must be above 0");
     TORCH_CHECK_VALUE(weight.dim() == 1 && weight.size(0) == D && weight.is_contiguous(), op,
                       ": weight must be a contiguous [", D, "], got ", weight.sizes());
     TORCH_CHECK_VALUE(group < 0 || group == 0 || group == 128, op, ": group must be 0 (per row) or 128, got ", group);

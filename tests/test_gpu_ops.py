@@ -200,6 +200,13 @@ def test_norm_long(skg):
         assert ((y[rows].double() - ref).abs() <= ref.abs() * (BF16 + (D / 2 + 16) * F32)).all()
 
 
+@pytest.mark.parametrize("quant", [None, "row", "group"])
+def test_norm_beyond_the_cache(skg, quant):
+    """More bytes than the last cache holds, where the kernels use the non-temporal hint."""
+    for D in (4096, 4091):
+        check_norm(skg, 7001, D, quant, True, seed=D)
+
+
 # ---- projections ------------------------------------------------------------
 
 def act_ref(z, act):
@@ -352,6 +359,32 @@ def test_linear_residual_in_place(skg, M, mode):
 def test_linear_large(skg, M, N, K, mode):
     check_linear(skg, M, N, K, mode, bias=True, residual=True, seed=M)
     check_linear(skg, M, N // 2, K, mode, gated=True, act="silu", seed=M)
+
+
+def test_linear_long_outputs(skg):
+    """More outputs than 31 bits hold: rows at both ends."""
+    M, N, K = 70001, 32768, 64
+    x = torch.randn(M, K, generator=gen(1), device="cuda").to(torch.bfloat16)
+    w = torch.randn(N, K, generator=gen(2), device="cuda").to(torch.bfloat16)
+    y = skg.linear(x, w)
+    for rows in (slice(0, 2), slice(M - 2, M)):
+        ref = x[rows].double() @ w.double().t().contiguous()
+        mag = x[rows].double().abs() @ w.double().abs().t().contiguous()
+        assert ((y[rows].double() - ref).abs() <= ref.abs() * BF16 + 2 * (2 * K + 64) * F32 * mag).all()
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_linear_long_weight(skg, M):
+    """A weight of more than 2^31 elements: its first and last features."""
+    N, K = 530000, 4096
+    w = torch.empty(N, K, dtype=torch.bfloat16, device="cuda")
+    w.random_(-4, 5, generator=gen(3))
+    x = torch.randn(M, K, generator=gen(4), device="cuda").to(torch.bfloat16)
+    y = skg.linear(x, w, out_dtype=torch.float32)
+    for part in (slice(0, 70), slice(N - 70, N)):
+        ref = x.double() @ w[part].double().t().contiguous()
+        mag = x.double().abs() @ w[part].double().abs().t().contiguous()
+        assert ((y[:, part].double() - ref).abs() <= (2 * K + 64) * F32 * mag).all()
 
 
 @pytest.mark.parametrize("mode", MODES)
