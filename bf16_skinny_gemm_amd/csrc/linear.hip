@@ -103,7 +103,8 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // unit takes into LDS, at 97.5 KB/us; and the round trips of 0.93 us that its waves wait
 // for one after another (a ring of two stages hides a part of them). A part of all three
 // is paid beside the largest, since they overlap incompletely, and each turn of blocks
-// adds its start and the sum of its waves. That of a tiled kernel is its time per stage.
+// adds its start and the sum of its waves. That of a tiled kernel is its time per stage
+// and the bytes of its outputs, which all blocks store together.
 // The constants were fitted to the times of 67 kernels at 932 sizes of each type (K 512
 // to 8192, N 256 to 12576, M 1 to 4096): the choice takes 2.2% longer than the best of
 // all kernels on average and 8% at the 90th percentile.
@@ -112,6 +113,7 @@ Choice choose(int mode, bool gated, bool exact, int M, int N, int64_t kbytes, in
     const int mats = gated ? 2 : 1;
     const double stages = (double)ceil_div(kbytes, 128);
     const double hbm = ((double)mats * N + M) * (double)kbytes / 22.5e6;
+    const double out = (double)M * N * 2.0 / 14.6e6;
     Choice best{};
     double least = 0.0;
     auto offer = [&](const Choice &c, double us) {
@@ -148,7 +150,7 @@ Choice choose(int mode, bool gated, bool exact, int M, int N, int64_t kbytes, in
         const TileKernel &k = t[i];
         const Choice c{k.fn, ceil_div(N, k.nb), ceil_div(M, k.bm), k.waves};
         const double per_cu = (double)ceil_div(c.nt * c.mt, cus);
-        offer(c, 8.2 + per_cu * (0.5 + stages * k.stage_us));
+        offer(c, 5.5 + per_cu * (0.5 + stages * k.stage_us) + out);
     }
     return best;
 }
@@ -184,7 +186,6 @@ int run_linear(const skinny_linear_t *p, bool fp8, hipStream_t stream)
     a.kb = (int)(((int64_t)p->K + 127) / 128);
     a.act = p->act;
     a.out_f32 = p->out_f32;
-    a.vec4 = out4_ok(*p);
 
     // the element-wise kernel loops over its tiles, so it takes any size
     auto launch_any = [&]() {

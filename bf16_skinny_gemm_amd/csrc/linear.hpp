@@ -5,12 +5,15 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ops_device.hpp"
 #include "skinny_ops.h"
 
 namespace skg {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
@@ -25,17 +28,16 @@ struct LinArgs {
     int M, N, K;               // K in elements
     int kb;                    // 128-column blocks of K (block scales)
     int act, out_f32;
-    int vec4;                  // four consecutive outputs, residuals and biases at a time
 };
 
-__device__ __forceinline__ float activate(float z, int act)
+template <int ACT>
+__device__ __forceinline__ float activate_as(float z)
 {
-    switch (act) {  // uniform: a scalar branch
-    case SKINNY_ACT_RELU:
+    if constexpr (ACT == SKINNY_ACT_RELU) {
         return z < 0.0f ? 0.0f : z;  // NaN stays
-    case SKINNY_ACT_SILU:
+    } else if constexpr (ACT == SKINNY_ACT_SILU) {
         return z * __builtin_amdgcn_rcpf(1.0f + __expf(-z));
-    case SKINNY_ACT_GELU: {
+    } else if constexpr (ACT == SKINNY_ACT_GELU) {
         // Phi(-|z|) = t (a1 + t (a2 + ..)) exp(-z^2 / 2) / 2 with t = 1 / (1 + p |z| / sqrt 2):
         // Abramowitz and Stegun 7.1.26, off by at most 7.5e-8. No cancellation for negative
         // z, and no call of erff, which took 0.4 us at the end of a decode-size launch.
@@ -45,15 +47,43 @@ __device__ __forceinline__ float activate(float z, int act)
                         t * 1.061405429f))));
         const float tail = 0.5f * q * __expf(-x * x);
         return z < 0.0f ? z * tail : z - z * tail;
-    }
-    case SKINNY_ACT_GELU_TANH: {
+    } else if constexpr (ACT == SKINNY_ACT_GELU_TANH) {
         // 0.5 (1 + tanh u) = 1 / (1 + exp(-2u)): no cancellation for negative z
         const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);
         return z * __builtin_amdgcn_rcpf(1.0f + __expf(-u2));
-    }
-    default:
+    } else {
         return z;
     }
+}
+
+// One scalar branch for all of a lane's values.
+template <int COUNT>
+__device__ __forceinline__ void activate(float (&z)[COUNT], int act)
+{
+    auto all = [&](auto ac) {
+#pragma unroll
+        for (int e = 0; e < COUNT; ++e)
+            z[e] = activate_as<decltype(ac)::value>(z[e]);
+    };
+    switch (act) {
+    case SKINNY_ACT_RELU:
+        return all(std::integral_constant<int, SKINNY_ACT_RELU>{});
+    case SKINNY_ACT_SILU:
+        return all(std::integral_constant<int, SKINNY_ACT_SILU>{});
+    case SKINNY_ACT_GELU:
+        return all(std::integral_constant<int, SKINNY_ACT_GELU>{});
+    case SKINNY_ACT_GELU_TANH:
+        return all(std::integral_constant<int, SKINNY_ACT_GELU_TANH>{});
+    default:
+        return;
+    }
+}
+
+__device__ __forceinline__ f32x4 activate4(f32x4 v, int act)
+{
+    float z[4] = {v[0], v[1], v[2], v[3]};
+    activate(z, act);
+    return f32x4{z[0], z[1], z[2], z[3]};
 }
 
 // One output from its sums: z of W0 (scaled), u of W1.
@@ -62,7 +92,9 @@ __device__ __forceinline__ float finish(const LinArgs &a, float z, float u, int 
 {
     if (a.bias[0])
         z += bf16_to_f32(a.bias[0][n]);
-    z = activate(z, a.act);
+    float act[1] = {z};
+    activate(act, a.act);
+    z = act[0];
     if constexpr (GATED) {
         if (a.bias[1])
             u += bf16_to_f32(a.bias[1][n]);
@@ -82,77 +114,133 @@ __device__ __forceinline__ void put(const LinArgs &a, float v, int m, int n)
         static_cast<uint16_t *>(a.y)[(int64_t)m * a.ldy + n] = f32_to_bf16(v);
 }
 
+__device__ __forceinline__ f32x4 widen4(u32x2 v) { return f32x4{lo_f32(v[0]), hi_f32(v[0]), lo_f32(v[1]), hi_f32(v[1])}; }
+
 // The residual of four consecutive outputs n .. n + 3 of row m, where finish4 wants it.
 __device__ __forceinline__ u32x2 residual4(const LinArgs &a, int m, int n)
 {
-    return a.res && a.vec4 && n + 4 <= a.N ? *reinterpret_cast<const u32x2 *>(a.res + (int64_t)m * a.ldr + n)
-                                           : u32x2{0, 0};
+    return a.res && n + 4 <= a.N ? *reinterpret_cast<const u32x2_any *>(a.res + (int64_t)m * a.ldr + n)
+                                 : u32x2{0, 0};
 }
 
-// Four consecutive outputs n .. n + 3 of row m, from sums that their scales have yet to
-// multiply (MODE 1), and their residual4.
+// Four consecutive outputs n .. n + 3 of row m, of which any may lie beyond N. The sums have
+// yet to be multiplied by their scales (MODE 1), xs that of the row.
 template <int MODE, bool GATED>
-__device__ __forceinline__ void finish4(const LinArgs &a, f32x4 z, f32x4 u, u32x2 r, int m, int n)
+__device__ __forceinline__ void finish4(const LinArgs &a, f32x4 z, f32x4 u, u32x2 r, float xs, int m, int n)
 {
-    if (a.vec4 && n + 4 <= a.N) {
-        if constexpr (MODE == 1) {
-            const float xs = a.xs[m];
-            const f32x4 s0 = *reinterpret_cast<const f32x4 *>(a.ws[0] + n);
+    if (n + 4 > a.N) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                z[e] *= xs * s0[e];
-            if constexpr (GATED) {
-                const f32x4 s1 = *reinterpret_cast<const f32x4 *>(a.ws[1] + n);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    u[e] *= xs * s1[e];
+        for (int e = 0; e < 4; ++e) {
+            if (n + e >= a.N)
+                continue;
+            float z1 = z[e], u1 = u[e];
+            if constexpr (MODE == 1) {
+                z1 *= xs * a.ws[0][n + e];
+                if constexpr (GATED)
+                    u1 *= xs * a.ws[1][n + e];
             }
+            put(a, finish<GATED>(a, z1, u1, m, n + e), m, n + e);
         }
-        if (a.bias[0]) {
-            const u32x2 b = *reinterpret_cast<const u32x2 *>(a.bias[0] + n);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                z[e] += e & 1 ? hi_f32(b[e >> 1]) : lo_f32(b[e >> 1]);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            z[e] = activate(z[e], a.act);
-        if constexpr (GATED) {
-            if (a.bias[1]) {
-                const u32x2 b = *reinterpret_cast<const u32x2 *>(a.bias[1] + n);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    u[e] += e & 1 ? hi_f32(b[e >> 1]) : lo_f32(b[e >> 1]);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                z[e] *= u[e];
-        } else if (a.res) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                z[e] += e & 1 ? hi_f32(r[e >> 1]) : lo_f32(r[e >> 1]);
-        }
-        const int64_t at = (int64_t)m * a.ldy + n;
-        if (a.out_f32)
-            *reinterpret_cast<f32x4 *>(static_cast<float *>(a.y) + at) = z;
-        else
-            *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(a.y) + at) =
-                u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
         return;
     }
+    if constexpr (MODE == 1) {
+        const f32x4 s0 = *reinterpret_cast<const f32x4_any *>(a.ws[0] + n);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (n + e >= a.N)
-            continue;
-        float z1 = z[e], u1 = u[e];
-        if constexpr (MODE == 1) {
-            z1 *= a.xs[m] * a.ws[0][n + e];
-            if constexpr (GATED)
-                u1 *= a.xs[m] * a.ws[1][n + e];
+        for (int e = 0; e < 4; ++e)
+            z[e] *= xs * s0[e];
+        if constexpr (GATED) {
+            const f32x4 s1 = *reinterpret_cast<const f32x4_any *>(a.ws[1] + n);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                u[e] *= xs * s1[e];
         }
-        put(a, finish<GATED>(a, z1, u1, m, n + e), m, n + e);
     }
+    if (a.bias[0])
+        z += widen4(*reinterpret_cast<const u32x2_any *>(a.bias[0] + n));
+    z = activate4(z, a.act);
+    if constexpr (GATED) {
+        if (a.bias[1])
+            u += widen4(*reinterpret_cast<const u32x2_any *>(a.bias[1] + n));
+        z *= u;
+    } else if (a.res) {
+        z += widen4(r);
+    }
+    const int64_t at = (int64_t)m * a.ldy + n;
+    if (a.out_f32)
+        *reinterpret_cast<f32x4_any *>(static_cast<float *>(a.y) + at) = z;
+    else
+        *reinterpret_cast<u32x2_any *>(static_cast<uint16_t *>(a.y) + at) =
+            u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
 }
+
+// The columns' part of the epilogue of the outputs n .. n + 7 <= N - 1, for many rows. A
+// load between a tile's stores would be waited for with all stores before it (loads and
+// stores share a counter): 4096 x 4096 outputs of K = 128 took 25 us that way, 15.8 so,
+// and 14.2 with stores that bypass the second-level cache, which they only pass through.
+template <int MODE, bool GATED>
+struct Columns8 {
+    f32x4 s[1 + GATED][2];
+    u32x2 b[1 + GATED][2];
+
+    __device__ __forceinline__ void load(const LinArgs &a, int n, bool wide)
+    {
+#pragma unroll
+        for (int q = 0; q < 1 + GATED; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (MODE == 1)
+                    s[q][h] = wide ? *reinterpret_cast<const f32x4_any *>(a.ws[q] + n + 4 * h) : f32x4{0, 0, 0, 0};
+                b[q][h] = wide && a.bias[q] ? *reinterpret_cast<const u32x2_any *>(a.bias[q] + n + 4 * h) : u32x2{0, 0};
+            }
+    }
+    // the loads have arrived
+    __device__ __forceinline__ void settle()
+    {
+#pragma unroll
+        for (int q = 0; q < 1 + GATED; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (MODE == 1)
+                    asm volatile("" : "+v"(s[q][h]));
+                asm volatile("" : "+v"(b[q][h]));
+            }
+    }
+    __device__ __forceinline__ void finish(const LinArgs &a, f32x4 (&z)[2], f32x4 (&u)[2], u32x4 r, int m, int n) const
+    {
+        float v[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (MODE == 1)
+                z[h] *= s[0][h];
+            z[h] += widen4(b[0][h]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[h * 4 + e] = z[h][e];
+        }
+        activate(v, a.act);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            z[h] = f32x4{v[h * 4], v[h * 4 + 1], v[h * 4 + 2], v[h * 4 + 3]};
+            if constexpr (GATED) {
+                if constexpr (MODE == 1)
+                    u[h] *= s[GATED][h];
+                z[h] *= u[h] + widen4(b[GATED][h]);
+            } else {
+                z[h] += widen4(u32x2{r[2 * h], r[2 * h + 1]});
+            }
+        }
+        const int64_t at = (int64_t)m * a.ldy + n;
+        if (a.out_f32) {
+            f32x4_any *y = reinterpret_cast<f32x4_any *>(static_cast<float *>(a.y) + at);
+            __builtin_nontemporal_store(z[0], y);
+            __builtin_nontemporal_store(z[1], y + 1);
+        } else {
+            const u32x4 y = {pack_bf16(z[0][0], z[0][1]), pack_bf16(z[0][2], z[0][3]), pack_bf16(z[1][0], z[1][1]),
+                             pack_bf16(z[1][2], z[1][3])};
+            __builtin_nontemporal_store(y, reinterpret_cast<u32x4_any *>(static_cast<uint16_t *>(a.y) + at));
+        }
+    }
+};
 
 // D[i][j] += sum_k A[i][k] B[j][k] for 16 x 16 outputs. A lane holds, of its row
 // (lane % 16) of A and of B, the LB * 16 bytes that the same lane of the other operand

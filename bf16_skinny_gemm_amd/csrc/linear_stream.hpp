@@ -183,7 +183,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
             if constexpr (GATED)
                 u += HALF ? part[(k * TM + j) * 64 + 32 + l] : part[((k * TN + TF + i) * TM + j) * 64 + l];
         }
-        finish4<MODE, GATED>(a, z, u, r, m, n);
+        finish4<MODE, GATED>(a, z, u, r, MODE == 1 ? a.xs[m] : 1.0f, m, n);
     }
 }
 

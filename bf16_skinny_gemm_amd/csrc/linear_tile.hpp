@@ -2,10 +2,10 @@
 // through LDS and shared by the block's waves.
 //
 // A stage is 128 bytes of K (64 bfloat16 or 128 e4m3: one block of scales) of the block's
-// rows of W and x, fetched by buffer loads that write LDS directly into one of two
-// buffers. The loads write LDS in lane order, so the layout is chosen by what each lane
-// asks for: piece j (16 bytes) of row r lies at position j ^ (r % 8) of the row's 128
-// bytes, and the 16-byte operand reads of eight neighbouring rows touch every bank once.
+// rows of W and x, fetched by buffer loads that write LDS directly, in lane order, so the
+// layout is chosen by what each lane asks for: piece j (16 bytes) of row r lies at position
+// j ^ (r % 8) of the row's 128 bytes, and the 16-byte operand reads of eight neighbouring
+// rows touch every bank once.
 //
 // W is the A operand (rows of D) and x the B operand (columns), so a lane holds four
 // consecutive output features of one row of y. A wave multiplies TN x TM fragments; per
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
     const int q8 = total / 8, r8 = total % 8;
     const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
     const int t = xcd * q8 + (xcd < r8 ? xcd : r8) + at;
-    constexpr int GROUP = BN * BM >= 65536 ? 4 : 8;  // 4096^3: 121 us against 128 with 8
+    constexpr int GROUP = BN * BM >= 65536 ? 4 : 8;  // 4096^3 took 121 us against 128 with 8
     const int per = GROUP * nt;
     const int first = t / per * GROUP;
     const int rows = mt - first < GROUP ? mt - first : GROUP;
@@ -248,16 +248,43 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
     }
 
     // The sums go through LDS, so that a wave stores whole rows of the tile: straight from
-    // the registers a store instruction covers 32 bytes of each of 16 rows, and the tile
-    // of 256 x 256 spent 30 us of 4096^3's 128 outside its stages. Piece p (4 outputs) of row
+    // the registers a store instruction covers 32 bytes of each of 16 rows. Outside its
+    // stages the tile of 256 x 256 spends 12 us of 4096^3's 95 this way, 30 without. Piece p (4 outputs) of row
     // r lies at position p ^ (r % 16), so neither side meets on a bank.
     constexpr int SMEM = WBUFS * WBUF + XBUFS * XBUF + WAVES * XBUFS * SBUF;
     constexpr int PASSES = BN * BM * 4 > SMEM ? 2 : 1;
     constexpr int JP = TM / PASSES, RP = WM * JP * 16;  // fragments per wave, rows per pass
-    constexpr int PL = NB / 4;                          // lanes per row
-    constexpr int RI = 64 / PL, ITERS = RP / (RI * WAVES), BATCH = ITERS < 4 ? ITERS : 4;
-    static_assert(PL <= 64 && RP % (RI * WAVES) == 0 && ITERS % BATCH == 0, "rows per wave");
-    const int pl = lane % PL, sub = lane / PL, n = n0 + pl * 4;
+    constexpr int PL = NB / 8;                          // lanes per row, 8 outputs each
+    constexpr int RI = 64 / PL, ITERS = RP / (RI * WAVES);
+    static_assert(PL <= 64 && RP % (RI * WAVES) == 0 && ITERS % 2 == 0, "rows per wave");
+    const int pl = lane % PL, sub = lane / PL, n = n0 + pl * 8;
+    const bool wide = n + 8 <= a.N;
+    Columns8<MODE, GATED> cols;
+    cols.load(a, n, wide);
+    // row k of this lane in pass q; its residuals are loaded before the first store, too
+    auto row_of = [&](int k) { return (k * WAVES + wave) * RI + sub; };
+    auto m_of = [&](int q, int row) { return m0 + (row / (JP * 16) * TM + q * JP) * 16 + row % (JP * 16); };
+    u32x4 res[GATED ? 1 : PASSES * ITERS];
+    if constexpr (!GATED)
+        if (a.res) {
+#pragma unroll
+            for (int k = 0; k < PASSES * ITERS; ++k) {
+                const int m = m_of(k / ITERS, row_of(k % ITERS));
+                res[k] = m < a.M && wide ? *reinterpret_cast<const u32x4_any *>(a.res + (int64_t)m * a.ldr + n)
+                                         : u32x4{0, 0, 0, 0};
+            }
+        }
+    if constexpr (MODE == 1) {
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            const int m = m0 + (wm * TM + j) * 16 + i16;
+            const float xs = m < a.M ? a.xs[m] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+                acc[i][j] *= xs;
+        }
+    }
+    cols.settle();
     stage_wait();  // the loads past the last stage have written their zeros
     static_for<0, PASSES>([&](auto qc) {
         constexpr int q = decltype(qc)::value;
@@ -272,25 +299,51 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
             });
         });
         __syncthreads();
-        for (int b = 0; b < ITERS; b += BATCH) {
-            int m[BATCH];
-            u32x2 res[BATCH];
+        auto sums = [&](int row, f32x4 (&z)[2], f32x4 (&u)[2]) {
+            const uint8_t *at_row = smem + row * (BN * 4);
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int row = ((b + k) * WAVES + wave) * RI + sub;
-                m[k] = m0 + (row / (JP * 16) * TM + q * JP) * 16 + row % (JP * 16);
-                res[k] = m[k] < a.M ? residual4(a, m[k], n) : u32x2{0, 0};
+            for (int h = 0; h < 2; ++h) {
+                z[h] = *reinterpret_cast<const f32x4 *>(at_row + ((pl * 2 + h) ^ (row & 15)) * 16);
+                u[h] = GATED ? *reinterpret_cast<const f32x4 *>(at_row + ((NB / 4 + pl * 2 + h) ^ (row & 15)) * 16) : z[h];
             }
+        };
+        if (GATED || !a.res) {
+#pragma unroll 2
+            for (int k = 0; k < ITERS; ++k) {
+                const int row = row_of(k), m = m_of(q, row);
+                f32x4 z[2], u[2];
+                sums(row, z, u);
+                if (m < a.M && wide)
+                    cols.finish(a, z, u, u32x4{0, 0, 0, 0}, m, n);
+            }
+        } else if constexpr (!GATED) {
+            if constexpr (q == 0)
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int row = ((b + k) * WAVES + wave) * RI + sub;
-                const uint8_t *at_row = smem + row * (BN * 4);
-                const f32x4 z = *reinterpret_cast<const f32x4 *>(at_row + (pl ^ (row & 15)) * 16);
-                const f32x4 u = GATED ? *reinterpret_cast<const f32x4 *>(at_row + ((PL + pl) ^ (row & 15)) * 16) : z;
-                if (m[k] < a.M && n < a.N)
-                    finish4<MODE, GATED>(a, z, u, res[k], m[k], n);
+                for (int k = 0; k < PASSES * ITERS; ++k)
+                    asm volatile("" : "+v"(res[k]));
+#pragma unroll
+            for (int k = 0; k < ITERS; ++k) {
+                const int row = row_of(k), m = m_of(q, row);
+                f32x4 z[2], u[2];
+                sums(row, z, u);
+                if (m < a.M && wide)
+                    cols.finish(a, z, u, res[q * ITERS + k], m, n);
             }
         }
+        if (vn % 8)  // the columns behind the last eight
+#pragma unroll 1
+            for (int o = threadIdx.x; o < RP * 8; o += WAVES * 64) {
+                const int row = o / 8, m = m_of(q, row), c = (vn & ~7) + o % 8;
+                const float *at = reinterpret_cast<const float *>(smem + row * (BN * 4) + c % 4 * 4);
+                if (c < vn && m < a.M) {
+                    float z = at[(c / 4 ^ (row & 15)) * 4], u = at[((NB * GATED + c) / 4 ^ (row & 15)) * 4];
+                    if constexpr (MODE == 1) {
+                        z *= a.ws[0][n0 + c];
+                        u *= a.ws[GATED][n0 + c];
+                    }
+                    put(a, finish<GATED>(a, z, u, m, n0 + c), m, n0 + c);
+                }
+            }
     });
 }
 
@@ -315,12 +368,12 @@ int tile_set(TileKernel *out)
     if constexpr (EXACT) {  // for float32 outputs only: one tile serves them
         out[n++] = tile_of<MODE, EXACT, GATED, 2, 2, 4, 4>(1.2f);
     } else if constexpr (MODE == 2) {
-        out[n++] = tile_of<MODE, EXACT, GATED, 2, 2, 4, 4>(0.82f);
-        out[n++] = tile_of<MODE, EXACT, GATED, 4, 2, 4, 4>(1.21f);
+        out[n++] = tile_of<MODE, EXACT, GATED, 2, 2, 4, 4>(0.76f);
+        out[n++] = tile_of<MODE, EXACT, GATED, 4, 2, 4, 4>(0.87f);
     } else {
-        out[n++] = tile_of<MODE, EXACT, GATED, 2, 2, 4, 4>(MODE ? 0.69f : 0.59f);
-        out[n++] = tile_of<MODE, EXACT, GATED, 4, 2, 4, 4>(1.17f);
-        out[n++] = tile_of<MODE, EXACT, GATED, 2, 4, 8, 4>(1.6f);
+        out[n++] = tile_of<MODE, EXACT, GATED, 2, 2, 4, 4>(MODE ? 0.63f : 0.5f);
+        out[n++] = tile_of<MODE, EXACT, GATED, 4, 2, 4, 4>(MODE ? 0.72f : 0.89f);
+        out[n++] = tile_of<MODE, EXACT, GATED, 2, 4, 8, 4>(MODE ? 1.3f : 1.44f);
     }
     return n;
 }

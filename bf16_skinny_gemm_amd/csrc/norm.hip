@@ -95,11 +95,6 @@ __device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d
     return (unsigned)v;
 }
 
-// Vectors in memory at any alignment: global memory takes unaligned 16-byte accesses, so
-// rows of odd width or stride move in the same instructions as aligned ones.
-typedef u32x4 __attribute__((aligned(1))) u32x4_any;
-typedef u32x2 __attribute__((aligned(1))) u32x2_any;
-
 // Eight bfloat16 values from p, of which `left` (> 0) exist: the others are 0. NT: with
 // the non-temporal hint.
 template <bool NT>

@@ -19,4 +19,9 @@ __device__ __forceinline__ unsigned pack_bf16(float a, float b)
     return __builtin_bit_cast(unsigned, __builtin_convertvector(v, bf16x2_t));
 }
 
+// Vectors in memory at any alignment: global memory takes unaligned 16-byte accesses, so
+// rows of odd width or stride move in the same instructions as aligned ones.
+typedef u32x4 __attribute__((aligned(1))) u32x4_any;
+typedef u32x2 __attribute__((aligned(1))) u32x2_any;
+
 }  // namespace skg

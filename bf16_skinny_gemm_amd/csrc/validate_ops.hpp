@@ -171,13 +171,4 @@ inline bool linear_vector_ok(const skinny_linear_t &a, bool fp8)
            aligned(a.W1, 16) && a.ldx <= (INT64_C(1) << 22) && a.K <= (1 << 22);
 }
 
-// Four consecutive outputs of a row can be stored at once, with their residuals, biases
-// and row scales loaded the same way.
-inline bool out4_ok(const skinny_linear_t &a)
-{
-    return aligned(a.y, a.out_f32 ? 16 : 8) && a.ldy % 4 == 0 && aligned(a.bias0, 8) && aligned(a.bias1, 8) &&
-           (!a.residual || (aligned(a.residual, 8) && a.ldr % 4 == 0)) &&
-           (a.scales != SKINNY_SCALES_ROW || (aligned(a.w0_scale, 16) && aligned(a.w1_scale, 16)));
-}
-
 }  // namespace skg_host

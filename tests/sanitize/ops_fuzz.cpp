@@ -74,10 +74,8 @@ int main()
         a.scales = (int32_t)pick({0, 1, 2});
         const bool ok = skg_host::validate_linear(&a, i & 1) == SKINNY_OK;
         accepted += ok;
-        if (ok) {
+        if (ok)
             (void)skg_host::linear_vector_ok(a, i & 1);
-            (void)skg_host::out4_ok(a);
-        }
     }
     // small calls in a crowded memory: what is accepted writes over no other operand
     long checked = 0;
