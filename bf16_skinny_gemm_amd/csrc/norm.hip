@@ -442,17 +442,17 @@ int run_norm(const skinny_norm_t *n, bool fp8, hipStream_t stream)
     const bool nt = bytes > (INT64_C(192) << 20);
     if (D <= 8192 && n->M <= 1024) {
         // few rows: one piece a lane and more waves a row; M = 64 x 4096 3.0 us against 3.5,
-        // 512 4.8 against 5, 2048 11.5 against 11.1
+        // 512 4.8 against 5, 2048 11.5 against 11.1. At most 1024 x 8192 x 8 bytes: never nt
         if (D <= 512)
-            fn = norm_fn<1, 1>(res, out, nt), wpr = 1;
+            fn = norm_fn_of<1, 1, false>(res, out), wpr = 1;
         else if (D <= 1024)
-            fn = norm_fn<2, 1>(res, out, nt), wpr = 2;
+            fn = norm_fn_of<2, 1, false>(res, out), wpr = 2;
         else if (D <= 2048)
-            fn = norm_fn<4, 1>(res, out, nt), wpr = 4;
+            fn = norm_fn_of<4, 1, false>(res, out), wpr = 4;
         else if (D <= 4096)
-            fn = norm_fn<8, 1>(res, out, nt), wpr = 8;
+            fn = norm_fn_of<8, 1, false>(res, out), wpr = 8;
         else
-            fn = norm_fn<16, 1>(res, out, nt), wpr = 16;
+            fn = norm_fn_of<16, 1, false>(res, out), wpr = 16;
     } else if (D <= 512) {
         fn = norm_fn<1, 1>(res, out, nt), wpr = 1;
     } else if (D <= 1024) {
