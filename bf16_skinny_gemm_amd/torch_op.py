@@ -281,7 +281,8 @@ def _norm_forward(self, x):
     if (w is not None and w.dim() == 1 and x.dim() >= 1 and x.shape[-1] == w.shape[0] and x.numel() > 0
             and x.dtype == w.dtype == torch.bfloat16 and x.device.type == "cuda" and w.device == x.device
             and w.is_contiguous() and _inference(x, w) and _device_is_gfx950(x.device)):
-        eps = self.eps if self.eps is not None else torch.finfo(x.dtype).eps
+        # without an eps the module adds float32's, for bfloat16 inputs too
+        eps = self.eps if self.eps is not None else torch.finfo(torch.float32).eps
         return rms_norm(x, w, eps)
     return type(self).forward(self, x)
 
@@ -290,18 +291,21 @@ def install(module: torch.nn.Module, fallback: bool = True, fused: bool = False)
     """Route the forward of every nn.Linear inside ``module`` through
     :func:`skinny_linear`. With ``fused``, layers with a bias and up to 64 rows of input
     run on linear_act and nn.RMSNorm modules on rms_norm, both where no gradient is asked
-    for. Returns the number of modules hooked."""
+    for; classes with a forward of their own keep it, and layers that an earlier call
+    hooked without ``fused`` take it up. Returns the number of modules hooked."""
     count = 0
     for sub in module.modules():
+        if fused and type(sub).forward is torch.nn.Linear.forward:
+            sub._skinny_fused = True
         if getattr(sub, "_skinny_hooked", False):
             continue
         if isinstance(sub, torch.nn.Linear):
-            def fwd(self, inp, _fallback=fallback, _fused=fused):
-                if _fused and self.bias is not None and qualifies_fused(inp, self.weight, self.bias):
+            def fwd(self, inp, _fallback=fallback):
+                if getattr(self, "_skinny_fused", False) and self.bias is not None and qualifies_fused(inp, self.weight, self.bias):
                     return linear_act(inp, self.weight, self.bias, None, "none", False)
                 return skinny_linear(inp, self.weight, self.bias, fallback=_fallback)
             sub.forward = functools.partial(fwd, sub)
-        elif fused and isinstance(sub, torch.nn.RMSNorm):
+        elif fused and type(sub).forward is torch.nn.RMSNorm.forward:
             sub.forward = functools.partial(_norm_forward, sub)
         else:
             continue

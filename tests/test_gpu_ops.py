@@ -361,6 +361,15 @@ def test_linear_large(skg, M, N, K, mode):
     check_linear(skg, M, N // 2, K, mode, gated=True, act="silu", seed=M)
 
 
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("M,N,ldy", [(1500, 1031, 1031), (2100, 516, 523), (700, 2047, 2048), (1025, 769, 771)])
+def test_linear_rows_that_end_inside_a_store(skg, M, N, ldy, mode):
+    check_linear(skg, M, N, 384, mode, act="gelu", bias=True, residual=True, ldy=ldy, seed=N)
+    check_linear(skg, M, N, 256, mode, residual=True, in_place=True, ldy=ldy, seed=N + 1)
+    check_linear(skg, M, N, 256, mode, bias=True, residual=True, f32=True, ldy=ldy, seed=N + 2)
+    check_linear(skg, M, N, 384, mode, gated=True, act="silu", bias=True, ldy=ldy, seed=N + 3)
+
+
 def test_linear_long_outputs(skg):
     """More outputs than 31 bits hold: rows at both ends."""
     M, N, K = 70001, 32768, 64
@@ -561,7 +570,7 @@ def test_install_fused(ops):
     assert ops.install(model, fused=True) == 4 and ops.install(model, fused=True) == 0
     norm0, lin0, lin1, norm1 = model
     with torch.no_grad():
-        a = ops.rms_norm(x, norm0.weight, torch.finfo(torch.bfloat16).eps)
+        a = ops.rms_norm(x, norm0.weight, torch.finfo(torch.float32).eps)
         b = ops.linear_act(a, lin0.weight, lin0.bias)
         c = torch.nn.functional.linear(b, lin1.weight)  # 15 rows: not the skinny product's
         assert torch.equal(model(x), ops.rms_norm(c, norm1.weight, 1e-5))
@@ -576,3 +585,48 @@ def test_install_fused(ops):
     y = model(x)
     y.float().sum().backward()
     assert lin0.weight.grad is not None and norm0.weight.grad is not None and lin0.bias.grad is not None
+
+
+def test_install_fused_default_eps(ops):
+    """A module without an eps, on rows small enough for it to count: both paths agree."""
+    norm = torch.nn.RMSNorm(256).cuda().to(torch.bfloat16)
+    x = torch.cat([torch.randn(4, 256, generator=gen(1), device="cuda") * s for s in (1.0, 0.05, 1e-3, 1e-4)])
+    x = x.to(torch.bfloat16)
+    with torch.no_grad():
+        plain = norm(x).double()
+        assert ops.install(norm, fused=True) == 1
+        got = norm(x).double()
+    # one rounding to bfloat16 each of values that float32 holds to (D / 2 + 16) of its steps
+    assert ((got - plain).abs() <= plain.abs() * (2 * BF16 + 2 * (128 + 16) * F32)).all()
+
+
+def test_install_fused_twice_and_own_forward(ops):
+    class OnePlus(torch.nn.RMSNorm):
+        def forward(self, x):
+            return torch.nn.functional.rms_norm(x, (64,), 1 + self.weight, 1e-6)
+
+    class Doubled(torch.nn.Linear):
+        def forward(self, x):
+            return 2 * super().forward(x)
+
+    model = torch.nn.Sequential(torch.nn.Linear(128, 64), OnePlus(64), Doubled(64, 64)).cuda().to(torch.bfloat16)
+    assert ops.install(model) == 2 and ops.install(model, fused=True) == 0
+    x = torch.randn(20, 128, generator=gen(2), device="cuda").to(torch.bfloat16)
+    with torch.no_grad():
+        y = model[0](x)
+        assert torch.equal(y, ops.linear_act(x, model[0].weight, model[0].bias, None, "none", False))
+        assert torch.equal(model[1](y), torch.nn.functional.rms_norm(y, (64,), 1 + model[1].weight, 1e-6))
+
+
+@pytest.mark.parametrize("quant", [None, "row", "group"])
+def test_norm_in_place_beyond_the_registers(skg, quant):
+    D = 33000
+    x = torch.randn(3, D, generator=gen(5), device="cuda").to(torch.bfloat16)
+    r = torch.randn(3, D, generator=gen(6), device="cuda").to(torch.bfloat16)
+    w = torch.randn(D, generator=gen(7), device="cuda").to(torch.bfloat16)
+    want = skg.rms_norm(x, w, residual=r, quant=quant)
+    for over in ("residual", "x"):
+        xc, rc = x.clone(), r.clone()
+        got = skg.rms_norm(xc, w, residual=rc, quant=quant, residual_out=rc if over == "residual" else xc)
+        assert all(torch.equal(bits(a) if a.dtype != torch.float32 else a, bits(b) if b.dtype != torch.float32 else b)
+                   for a, b in zip(got, want))
