@@ -105,9 +105,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // is paid beside the largest, since they overlap incompletely, and each turn of blocks
 // adds its start and the sum of its waves. That of a tiled kernel is its time per stage
 // and the bytes of its outputs, which all blocks store together.
-// The constants were fitted to the times of 67 kernels at 932 sizes of each type (K 512
-// to 8192, N 256 to 12576, M 1 to 4096): the choice takes 2.2% longer than the best of
-// all kernels on average and 8% at the 90th percentile.
+// The constants were fitted to the times of some 80 kernels at 1228 sizes of each type (K
+// 512 to 8192, N 256 to 12576, M 17 to 4096): the choice takes 2.0% longer than the best of
+// all kernels on average and 7% at the 90th percentile.
 Choice choose(int mode, bool gated, bool exact, int M, int N, int64_t kbytes, int cus)
 {
     const int mats = gated ? 2 : 1;

@@ -309,7 +309,7 @@ struct StreamKernel {
     const void *fn;
     int nb, bm, ring, waves, stage, lds, tiles;
 };
-constexpr int kStreamMost = 8;  // kernels of one set
+constexpr int kStreamMost = 10;  // kernels of one set
 
 // A kernel of linear_tile.hpp: outputs per block along N and M, waves, and a stage's time
 // (microseconds, blocks of one compute unit one after another).
@@ -318,7 +318,7 @@ struct TileKernel {
     int nb, bm, waves;
     float stage_us;
 };
-constexpr int kTileMost = 4;
+constexpr int kTileMost = 5;
 
 // The kernels that take M rows, by element type and scales; returns their number.
 int stream_kernels_bf16(int M, bool gated, bool exact, StreamKernel *out);

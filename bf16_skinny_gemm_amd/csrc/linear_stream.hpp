@@ -32,12 +32,13 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
     constexpr int BN = NB * MATS, BM = TM * 16;
     constexpr int TN = (BN + 15) / 16;          // instructions along the rows of W
     constexpr int TF = HALF ? 1 : NB / 16;      // and along those of one weight
-    constexpr int SCALES = (BN + XR) * 128;     // offset of a stage's scales: 64 of x, then of each weight
-    constexpr int STAGE = SCALES + (BLOCK ? (1 + MATS) * 256 : 0);
-    constexpr int LOADS = (BN + XR) / 8 + (BLOCK ? 1 + MATS : 0);  // of one wave and stage
+    constexpr int XS = (BM + 63) / 64;          // loads of x's scales, 64 each
+    constexpr int SCALES = (BN + XR) * 128;     // offset of a stage's scales: of x, then of each weight
+    constexpr int STAGE = SCALES + (BLOCK ? (XS + MATS) * 256 : 0);
+    constexpr int LOADS = (BN + XR) / 8 + (BLOCK ? XS + MATS : 0);  // of one wave and stage
     constexpr int PART = WAVES * TN * TM * 1024;  // the waves' sums, after the last stage
     constexpr int SMEM = PART > WAVES * RING * STAGE ? PART : WAVES * RING * STAGE;
-    static_assert(XR <= BM && BM <= 64 && NB <= 64, "tile");
+    static_assert(XR <= BM && 128 % NB == 0, "tile");
     __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM];
 
     const int lane = threadIdx.x & 63;
@@ -89,10 +90,14 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
             load_to_lds(xr, in ? (unsigned)(c * 8 + lrow) * (unsigned)a.ldx + k : kOutOfRange,
                         lds + (unsigned)(BN + c * 8) * 128u);
         if constexpr (BLOCK) {
-            load4_to_lds(xsr, lane < vm ? (unsigned)(lane * a.kb + s) * 4u : kOutOfRange, lds + SCALES);
+#pragma unroll
+            for (int c = 0; c < XS; ++c) {
+                const int m = c * 64 + lane;
+                load4_to_lds(xsr, m < vm ? (unsigned)(m * a.kb + s) * 4u : kOutOfRange, lds + SCALES + 256u * c);
+            }
 #pragma unroll
             for (int q = 0; q < MATS; ++q)
-                load4_to_lds(wsr[q], (unsigned)s * 4u, lds + SCALES + 256u * (1 + q));
+                load4_to_lds(wsr[q], (unsigned)s * 4u, lds + SCALES + 256u * (XS + q));
         }
     };
 
@@ -135,7 +140,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
             for (int i = 0; i < TN; ++i)
 #pragma unroll
                 for (int j = 0; j < TM; ++j)
-                    sc[i][j] = f[j * 16 + i16] * f[64 * (1 + (HALF && GATED ? g >> 1 : i / TF)) + lane];
+                    sc[i][j] = f[j * 16 + i16] * f[64 * (XS + (HALF && GATED ? g >> 1 : i / TF)) + lane];
         }
         lds_read_wait();  // the stage is in registers: its slot may be written again
         if (s + RING * WAVES < stages)
@@ -195,7 +200,7 @@ template <int MODE, bool EXACT, bool GATED, int NB, int TM, int XR, int RING, in
 StreamKernel stream_of()
 {
     constexpr int MATS = GATED ? 2 : 1, BN = NB * MATS, TN = (BN + 15) / 16;
-    constexpr int STAGE = (BN + XR) * 128 + (MODE == 2 ? (1 + MATS) * 256 : 0);
+    constexpr int STAGE = (BN + XR) * 128 + (MODE == 2 ? ((TM + 3) / 4 + MATS) * 256 : 0);
     constexpr int RINGS = WAVES * RING * STAGE, PART = WAVES * TN * TM * 1024;
     return StreamKernel{
         reinterpret_cast<const void *>(&skg::linear_stream_kernel<MODE, EXACT, GATED, NB, TM, XR, RING, WAVES, NT>),
@@ -226,12 +231,15 @@ int stream_set(int M, StreamKernel *out)
         out[n++] = stream_of<MODE, EXACT, GATED, 32, 2, 32, 2, 4, false>();
         out[n++] = stream_of<MODE, EXACT, GATED, 32, 4, 64, 1, 4, false>();
         out[n++] = stream_of<MODE, EXACT, GATED, 32, 4, 64, 1, 8, false>();
+        if constexpr (!(EXACT && MODE == 2))  // where the registers hold it
+            out[n++] = stream_of<MODE, EXACT, GATED, GATED ? 32 : 64, 6, 96, 1, 6, false>();
         if constexpr (!GATED) {
             out[n++] = stream_of<MODE, EXACT, GATED, 64, 3, 48, 1, 4, false>();
             out[n++] = stream_of<MODE, EXACT, GATED, 64, 4, 64, 1, 4, false>();
+            out[n++] = stream_of<MODE, EXACT, GATED, 64, 4, 64, 1, 8, false>();
         }
     }
-    static_assert(kStreamMost >= 8, "the largest set");
+    static_assert(kStreamMost >= 10, "the largest set");
     return n;
 }
 
