@@ -24,6 +24,11 @@
 // The loop over the stages has no branch (behind one, the compiler moved the sums between
 // the two register files at every step): stages past the last read zeros, since every
 // load past K does, and add nothing.
+//
+// Bound by the matrix pipe and its power limit: 4096^3 in bfloat16 95 us (1448 TF), 109 with
+// residual, activation and cold inputs; e4m3 with row scales 4096 x 4096 x 8192 in 103 (2670
+// TF). At the tiles of 128 x 128, by what a compute unit takes into LDS (32 KB a stage at
+// some 75 KB/us).
 #pragma once
 
 #include "lds_load.hpp"
