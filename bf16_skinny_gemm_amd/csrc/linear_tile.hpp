@@ -25,9 +25,9 @@
 // the two register files at every step): stages past the last read zeros, since every
 // load past K does, and add nothing.
 //
-// Bound by the matrix pipe and its power limit: 4096^3 in bfloat16 95 us (1448 TF), 109 with
-// residual, activation and cold inputs; e4m3 with row scales 4096 x 4096 x 8192 in 103 (2670
-// TF). At the tiles of 128 x 128, by what a compute unit takes into LDS (32 KB a stage at
+// Bound by the matrix pipe and its power limit: 4096^3 in bfloat16 95 to 110 us by the card
+// (1250 to 1450 TF), 106 to 110 with residual, activation and cold inputs; e4m3 with row
+// scales 4096 x 4096 x 8192 in 98 to 103 (2670 to 2800 TF). At the tiles of 128 x 128, by what a compute unit takes into LDS (32 KB a stage at
 // some 75 KB/us).
 #pragma once
 
@@ -254,8 +254,8 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
 
     // The sums go through LDS, so that a wave stores whole rows of the tile: straight from
     // the registers a store instruction covers 32 bytes of each of 16 rows. Outside its
-    // stages the tile of 256 x 256 spends 12 us of 4096^3's 95 this way, 30 without. Piece p (4 outputs) of row
-    // r lies at position p ^ (r % 16), so neither side meets on a bank.
+    // stages the tile of 256 x 256 spends 12 us of 4096^3 this way, 30 without. Piece p (4
+    // outputs) of row r lies at position p ^ (r % 16), so neither side meets on a bank.
     constexpr int SMEM = WBUFS * WBUF + XBUFS * XBUF + WAVES * XBUFS * SBUF;
     constexpr int PASSES = BN * BM * 4 > SMEM ? 2 : 1;
     constexpr int JP = TM / PASSES, RP = WM * JP * 16;  // fragments per wave, rows per pass

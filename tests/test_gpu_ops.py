@@ -630,3 +630,36 @@ def test_norm_in_place_beyond_the_registers(skg, quant):
         got = skg.rms_norm(xc, w, residual=rc, quant=quant, residual_out=rc if over == "residual" else xc)
         assert all(torch.equal(bits(a) if a.dtype != torch.float32 else a, bits(b) if b.dtype != torch.float32 else b)
                    for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("lead", [(5,), (2, 3)])
+def test_python_kernels_agree(ops, lead):
+    """The Python kernels of the operators, registered where the C++ ones are not built."""
+    g, K, N = gen(11), 256, 130
+    bf = torch.bfloat16
+    x, r = (torch.randn(*lead, K, generator=g, device="cuda").to(bf) for _ in range(2))
+    w, b, u = (torch.randn(*s, generator=g, device="cuda").to(bf) for s in ((K,), (N,), (N,)))
+    wg, wu = (torch.randn(N, K, generator=g, device="cuda").to(bf) for _ in range(2))
+    res = torch.randn(*lead, N, generator=g, device="cuda").to(bf)
+    qg, qu = (t.float().to(torch.float8_e4m3fn) for t in (wg, wu))
+    rows, blocks = torch.rand(N, generator=g, device="cuda"), torch.rand(2, 2, generator=g, device="cuda")
+    q0, s0 = ops.rms_norm_fp8(x, w, 1e-6, 0)
+    q1, s1 = ops.rms_norm_fp8(x, w, 1e-6, 128)
+    calls = {
+        "rms_norm": [(x, w, 1e-6)],
+        "add_rms_norm": [(x, r, w, 1e-6)],
+        "rms_norm_fp8": [(x, w, 1e-6, 0), (x, w, 1e-6, 128)],
+        "add_rms_norm_fp8": [(x, r, w, 1e-6, 0), (x, r, w, 1e-6, 128)],
+        "linear_act": [(x, wg), (x, wg, b, res, "gelu", True)],
+        "linear_gated": [(x, wg, wu), (x, wg, wu, b, u, "relu", True)],
+        "linear_fp8": [(q0, s0, qg, rows, b, res, "silu", False), (q1, s1, qg, blocks)],
+        "linear_gated_fp8": [(q0, s0, qg, rows, qu, rows, b, u), (q1, s1, qg, blocks, qu, blocks)],
+    }
+    assert set(calls) == set(ops._PY_KERNELS)
+    for name, several in calls.items():
+        for args in several:
+            want, got = getattr(ops, name)(*args), ops._PY_KERNELS[name](*args)
+            want, got = (want, got) if isinstance(want, (tuple, list)) else ((want,), (got,))
+            assert len(want) == len(got)
+            for a, c in zip(want, got):
+                assert a.dtype == c.dtype and a.shape == c.shape and torch.equal(bits(a), bits(c)), name
