@@ -1,8 +1,8 @@
 // The projection kernel for up to a few hundred rows of x: W streams from HBM through LDS
 // once, and K is split over the waves of a block.
 //
-// Every compute unit needs a part of W to stream, so the tiles of outputs are small (8 to
-// 64 a side). Shared between the waves of a block along K, such a tile needs no barrier
+// Every compute unit needs a part of W to stream, so the tiles of outputs are small (4 to
+// 96 a side). Shared between the waves of a block along K, such a tile needs no barrier
 // until its end: each wave fetches its own 128-byte parts of K (the tile's rows of W and
 // x) into its own ring of stages in LDS and multiplies the whole tile, waiting for its own
 // loads only, while the loads of its later stages and of the other waves are in flight.
@@ -22,7 +22,8 @@ namespace skg {
 // MODE: 0 bfloat16, 1 e4m3 with row scales, 2 e4m3 with block scales; EXACT: see
 // mfma_bytes. A block computes NB output features (of each
 // weight, GATED) of TM * 16 rows with WAVES waves. NB = 8 fills half of an instruction's
-// rows, or one half with each weight. A wave's part of LDS is a ring of RING stages; XR
+// rows, or one half with each weight; NB = 4 (GATED) both weights' rows in one half, for
+// N that fills too few compute units otherwise. A wave's part of LDS is a ring of RING stages; XR
 // rows of x are loaded (8 where M <= 8, else TM * 16: what other columns of the
 // instruction multiply reaches no output). NT: W is read with the non-temporal hint.
 template <int MODE, bool EXACT, bool GATED, int NB, int TM, int XR, int RING, int WAVES, bool NT>
@@ -30,14 +31,15 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
 {
     constexpr bool FP8 = MODE != 0, BLOCK = MODE == 2;
     constexpr int MATS = GATED ? 2 : 1;
-    constexpr bool HALF = NB == 8;
+    constexpr bool HALF = NB == 8, QUARTER = NB == 4;
+    static_assert(!QUARTER || GATED, "a load takes 8 rows");
     constexpr int BN = NB * MATS, BM = TM * 16;
     constexpr int TN = (BN + 15) / 16;          // instructions along the rows of W
-    constexpr int TF = HALF ? 1 : NB / 16;      // and along those of one weight
+    constexpr int TF = HALF || QUARTER ? 1 : NB / 16;      // and along those of one weight
     constexpr int XS = (BM + 63) / 64;          // loads of x's scales, 64 each
     constexpr int SCALES = (BN + XR) * 128;     // offset of a stage's scales: of x, then of each weight
     constexpr int STAGE = SCALES + (BLOCK ? (XS + MATS) * 256 : 0);
-    constexpr int LOADS = (BN + XR) / 8 + (BLOCK ? XS + MATS : 0);  // of one wave and stage
+    constexpr int LOADS = (QUARTER ? 2 : BN / 8) + XR / 8 + (BLOCK ? XS + MATS : 0);  // of one wave and stage
     constexpr int PART = WAVES * TN * TM * 1024;  // the waves' sums, after the last stage
     constexpr int SMEM = PART > WAVES * RING * STAGE ? PART : WAVES * RING * STAGE;
     static_assert(XR <= BM && 128 % NB == 0, "tile");
@@ -81,6 +83,13 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
         const unsigned k = (unsigned)s * 128u + piece;
         const bool in = k < (unsigned)KB;
         const unsigned lds = lds0 + (unsigned)(slot * STAGE);
+        if constexpr (QUARTER) {  // lane i writes at lds + 16 i, whichever lanes are off
+            const unsigned at = in ? (unsigned)(lrow & 3) * (unsigned)KB + k : kOutOfRange;
+            if (lane < 32)
+                load_to_lds<NT>(wr[0], at, lds);
+            else
+                load_to_lds<NT>(wr[MATS - 1], at, lds);
+        }
 #pragma unroll
         for (int q = 0; q < MATS; ++q)
 #pragma unroll
@@ -142,7 +151,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
             for (int i = 0; i < TN; ++i)
 #pragma unroll
                 for (int j = 0; j < TM; ++j)
-                    sc[i][j] = f[j * 16 + i16] * f[64 * (XS + (HALF && GATED ? g >> 1 : i / TF)) + lane];
+                    sc[i][j] = f[j * 16 + i16] * f[64 * (XS + (QUARTER ? g & 1 : HALF && GATED ? g >> 1 : i / TF)) + lane];
         }
         lds_read_wait();  // the stage is in registers: its slot may be written again
         if (s + RING * WAVES < stages)
@@ -176,7 +185,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
         for (int j = 0; j < TM; ++j)
             part[((wave * TN + i) * TM + j) * 64 + lane] = acc[i][j];
     __syncthreads();
-    constexpr int SLOTS = HALF ? 32 : 64;  // lanes that hold outputs (of the first weight)
+    constexpr int SLOTS = QUARTER ? 16 : HALF ? 32 : 64;  // lanes that hold outputs (of the first weight)
     for (int o = threadIdx.x; o < TF * TM * SLOTS; o += WAVES * 64) {
         const int l = o % SLOTS, j = o / SLOTS % TM, i = o / SLOTS / TM;
         const int m = m0 + j * 16 + (l & 15), n = n0 + i * 16 + (l >> 4) * 4;
@@ -188,7 +197,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
         for (int k = 0; k < WAVES; ++k) {
             z += part[((k * TN + i) * TM + j) * 64 + l];
             if constexpr (GATED)
-                u += HALF ? part[(k * TM + j) * 64 + 32 + l] : part[((k * TN + TF + i) * TM + j) * 64 + l];
+                u += HALF || QUARTER ? part[(k * TM + j) * 64 + SLOTS + l] : part[((k * TN + TF + i) * TM + j) * 64 + l];
         }
         finish4<MODE, GATED>(a, z, u, r, MODE == 1 ? a.xs[m] : 1.0f, m, n);
     }
@@ -221,11 +230,15 @@ int stream_set(int M, StreamKernel *out)
         out[n++] = stream_of<MODE, E, GATED, 8, 1, 8, 3, 8, true>();
         out[n++] = stream_of<MODE, E, GATED, 16, 1, 8, 2, 4, true>();
         out[n++] = stream_of<MODE, E, GATED, 16, 1, 8, 2, 8, true>();
+        if constexpr (GATED)  // 8 x 1024 x 8192 bfloat16 8.4 us against 10.0 with 8 features a block
+            out[n++] = stream_of<MODE, E, GATED, 4, 1, 8, 3, 8, true>();
     } else if (M <= 16) {
         out[n++] = stream_of<MODE, E, GATED, 8, 1, 16, 2, 8, true>();
         out[n++] = stream_of<MODE, E, GATED, 16, 1, 16, 2, 4, true>();
         out[n++] = stream_of<MODE, E, GATED, 16, 1, 16, 2, 8, true>();
         out[n++] = stream_of<MODE, E, GATED, 32, 1, 16, 2, 4, true>();
+        if constexpr (GATED)
+            out[n++] = stream_of<MODE, E, GATED, 4, 1, 16, 2, 8, true>();
     } else {
         out[n++] = stream_of<MODE, EXACT, GATED, 16, 1, 16, 1, 8, false>();
         out[n++] = stream_of<MODE, EXACT, GATED, 16, 2, 32, 2, 4, false>();
