@@ -43,8 +43,12 @@ __device__ __forceinline__ void stage_wait()
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(YOUNGER) : "memory");
 }
 
-// This wave's reads of LDS have returned.
-__device__ __forceinline__ void lds_read_wait() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// All but this wave's YOUNGER latest reads of LDS, which return in order, are there.
+template <int YOUNGER = 0>
+__device__ __forceinline__ void lds_read_wait()
+{
+    asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(YOUNGER) : "memory");
+}
 
 __device__ __forceinline__ u32x4 rsrc_words(const void *base, unsigned bytes)
 {
