@@ -23,7 +23,7 @@
 namespace skg {
 
 constexpr float kE4m3Max = 448.0f;
-constexpr float kLeastAmax = 0x1p-100f;  // keeps 448 / amax finite for a row of zeros
+constexpr float kLeastAmax = 0x1p-100f;  // keeps 1 / scale finite for a row or group of zeros
 
 struct NormArgs {
     const uint16_t *x, *r, *w;
@@ -79,15 +79,18 @@ __device__ __forceinline__ unsigned wave_umax(unsigned v)
 
 __device__ __forceinline__ unsigned abs_bits(float v) { return __builtin_bit_cast(unsigned, v) & 0x7FFFFFFFu; }
 
-// scale of the largest |y| (amax >= 0, or NaN); the reciprocal multiplies y.
+// scale of the largest |y| (amax >= 0, or NaN).
 __device__ __forceinline__ float scale_of(float amax)
 {
     const float a = amax < kLeastAmax ? kLeastAmax : amax;  // NaN stays
     return a / kE4m3Max;
 }
 
-// q = e4m3(hw * f), f = 1 / (rms * scale). |hw * f| <= 448 (1 + 2^-22) by the choice of
-// the scale, which rounds to 448, so no clamp is needed.
+// q = e4m3((hw * f) * (1 / scale)), f = 1 / rms. The factors stay apart: f / scale overflows
+// for rows of rms below 2^-19 whose scale is the least one, and their zeros would turn into
+// NaN; 1 / scale is at most 448 * 2^100. |q| <= 448 (1 + 2^-22) by the choice of the scale,
+// which rounds to 448, so no clamp is needed. Against a division by the scale the product
+// is off by at most 2 * 2^-24: a value on the border of two e4m3 ones may go to the other.
 __device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d)
 {
     int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
@@ -259,7 +262,7 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
         float sc = 0.0f, g = 0.0f;
         if constexpr (OUT == kOutRow) {
             sc = scale_of(__builtin_bit_cast(float, most) * f);
-            g = f / sc;
+            g = 1.0f / sc;
             if (t == 0)
                 a.scale[row] = sc;
         }
@@ -268,13 +271,13 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
             const int c = (p * LANES + t) * 8;
             if constexpr (OUT == kOutGroup) {
                 sc = scale_of(__builtin_bit_cast(float, umax16(top[p])) * f);
-                g = f / sc;
+                g = 1.0f / sc;
                 if ((lane & 15) == 0 && c < a.D)
                     a.scale[rr * a.groups + (c >> 7)] = sc;
             }
             u32x2 o;
-            o[0] = pack_e4m3(hw[p][0] * g, hw[p][1] * g, hw[p][2] * g, hw[p][3] * g);
-            o[1] = pack_e4m3(hw[p][4] * g, hw[p][5] * g, hw[p][6] * g, hw[p][7] * g);
+            o[0] = pack_e4m3(hw[p][0] * f * g, hw[p][1] * f * g, hw[p][2] * f * g, hw[p][3] * f * g);
+            o[1] = pack_e4m3(hw[p][4] * f * g, hw[p][5] * f * g, hw[p][6] * f * g, hw[p][7] * f * g);
             if (c < a.D)
                 store8<NT>(y + c, o, a.D - c);
         }
@@ -331,13 +334,13 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a)
     } else {
         uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.ldy;
         if constexpr (OUT == kOutRow) {
-            const float sc = scale_of(__builtin_bit_cast(float, most) * f), g = f / sc;
+            const float sc = scale_of(__builtin_bit_cast(float, most) * f), g = 1.0f / sc;
             if (t == 0)
                 a.scale[row] = sc;
             for (int64_t i = t; i < a.D; i += 256) {
                 const float h = h_at((int)i);
                 store_h((int)i, h);
-                y[i] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(h * bf16_to_f32(a.w[i]) * g, 0.0f, 0, false);
+                y[i] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(h * bf16_to_f32(a.w[i]) * f * g, 0.0f, 0, false);
             }
         } else {
             // a wave takes a group of 128 columns, two per lane
@@ -352,7 +355,7 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a)
                     const unsigned b = abs_bits(v[k]);
                     top = b > top ? b : top;
                 }
-                const float sc = scale_of(__builtin_bit_cast(float, wave_umax(top)) * f), g = f / sc;
+                const float sc = scale_of(__builtin_bit_cast(float, wave_umax(top)) * f), g = 1.0f / sc;
                 if (lane == 0)
                     a.scale[row * a.groups + g0] = sc;
 #pragma unroll
@@ -360,7 +363,7 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a)
                     const int64_t i = g0 * 128 + k * 64 + lane;
                     if (i < a.D) {
                         store_h((int)i, h[k]);
-                        y[i] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[k] * g, 0.0f, 0, false);
+                        y[i] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[k] * f * g, 0.0f, 0, false);
                     }
                 }
             }

@@ -64,7 +64,8 @@ int skinny_rms_norm_bf16(const skinny_norm_t *args, hipStream_t stream);
 
 /* y as e4m3 with float32 scales: scale = max(largest |y| of the row or group, 2^-100)
  * / 448 and q = e4m3(y / scale), nearest-even, so that q * scale stands for y. y is not
- * rounded before that. A NaN in a row makes the row's scales and values NaN. An infinity makes
+ * rounded to fewer bits before that; the quotient is y times the float32 reciprocal. Rows
+ * and groups of zeros give zeros (with eps == 0 a row of zeros is 0 / 0: NaN). A NaN in a row makes the row's scales and values NaN. An infinity makes
  * the scale of its row or group NaN with all its values, and the row's other groups 0. */
 int skinny_rms_norm_fp8(const skinny_norm_t *args, hipStream_t stream);
 

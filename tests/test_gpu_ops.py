@@ -663,3 +663,22 @@ def test_python_kernels_agree(ops, lead):
             assert len(want) == len(got)
             for a, c in zip(want, got):
                 assert a.dtype == c.dtype and a.shape == c.shape and torch.equal(bits(a), bits(c)), name
+
+
+@pytest.mark.parametrize("eps", [1e-6, 1e-12, 1e-20, 1e-30])
+@pytest.mark.parametrize("quant", ["row", "group"])
+@pytest.mark.parametrize("D", [256, 999, 4096, 20000, 33000])
+def test_norm_fp8_zeros_and_small_rows_at_any_eps(skg, D, quant, eps):
+    """Rows and groups of zeros stay zeros beside values of any size, at every eps above 0."""
+    x = torch.randn(9, D, generator=gen(D), device="cuda")
+    x[0] = 0.0
+    x[1] *= 1e-3
+    x[2:5] *= 1e-7
+    x[3, :128] = 0.0          # a group of zeros in a small row
+    x[4, 5:] = 0.0
+    x[5] *= 2.0 ** -60
+    x[6] *= 2.0 ** -115       # y below the least scale's at the larger eps
+    x[7, 128:] = 0.0
+    x = x.to(torch.bfloat16)
+    check_norm(skg, 9, D, quant, False, x=x, eps=eps, seed=D)
+    check_norm(skg, 9, D, quant, True, x=x, r=torch.zeros_like(x), eps=eps, seed=D)
