@@ -46,7 +46,7 @@ __device__ __forceinline__ float activate_as(float z)
         const float q = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f +
                         t * 1.061405429f))));
         const float tail = 0.5f * q * __expf(-x * x);
-        return z < 0.0f ? z * tail : z - z * tail;
+        return z * (z < 0.0f ? tail : 1.0f - tail);  // z - z * tail would be NaN at infinity
     } else if constexpr (ACT == SKINNY_ACT_GELU_TANH) {
         // 0.5 (1 + tanh u) = 1 / (1 + exp(-2u)): no cancellation for negative z
         const float u2 = 1.5957691216057308f * (z + 0.044715f * z * z * z);

@@ -682,3 +682,37 @@ def test_norm_fp8_zeros_and_small_rows_at_any_eps(skg, D, quant, eps):
     x = x.to(torch.bfloat16)
     check_norm(skg, 9, D, quant, False, x=x, eps=eps, seed=D)
     check_norm(skg, 9, D, quant, True, x=x, r=torch.zeros_like(x), eps=eps, seed=D)
+
+
+# rows, inputs and element types that take the streaming, the tiled and the element-wise kernel
+EPILOGUE_PATHS = [(3, 64, "bf16"), (5, 128, "row"), (40, 128, "block"), (600, 128, "bf16"), (600, 128, "row"),
+                  (600, 128, "block"), (3, 0, "bf16"), (6, 63, "row")]
+
+
+def act_of_values(skg, values, act, M, K, mode, f32):
+    """act of given bfloat16 values (the bias) through a product of zeros, [M, len(values)]."""
+    N = values.numel()
+    xv, wv, xs, ws, _, _ = make_linear(M, N, K, mode, 1, 1)
+    y = skg.linear(torch.zeros_like(xv.contiguous()), wv[0], bias=values, act=act, x_scale=xs,
+                   w_scale=ws[0] if ws else None, out_dtype=torch.float32 if f32 else torch.bfloat16)
+    assert torch.equal(bits(y), bits(y[:1].expand(M, N).contiguous()))
+    return y[0].double()
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M,K,mode", EPILOGUE_PATHS)
+def test_activations_of_infinite_large_and_nan_values(skg, M, K, mode, act):
+    inf = float("inf")
+    v = torch.tensor([inf, 3e38, 1e30, 1e10, 300.0, 0.0, -300.0, -1e10, -1e30, -3e38, float("nan"), -inf, 1.0],
+                     device="cuda").to(torch.bfloat16)
+    for f32 in (False, True):
+        y = act_of_values(skg, v, act, M, K, mode, f32)
+        assert torch.equal(y[:6], v[:6].double())  # act(z) = z to the last bit for large z
+        assert y[10].isnan()
+        if act == "none":
+            assert torch.equal(y[6:10], v[6:10].double()) and y[11] == -inf
+        else:
+            assert (y[6:10] == 0).all()
+            # -inf times the 0 that it is weighted with, but relu's selects
+            assert y[11] == 0 if act == "relu" else y[11].isnan()
+        assert abs(y[12] - act_ref(torch.ones((), dtype=torch.float64), act)) <= BF16
