@@ -716,3 +716,18 @@ def test_activations_of_infinite_large_and_nan_values(skg, M, K, mode, act):
             # -inf times the 0 that it is weighted with, but relu's selects
             assert y[11] == 0 if act == "relu" else y[11].isnan()
         assert abs(y[12] - act_ref(torch.ones((), dtype=torch.float64), act)) <= BF16
+
+
+@pytest.mark.parametrize("M,K,mode", EPILOGUE_PATHS)
+def test_gelu_is_right_relative_to_its_value(skg, M, K, mode):
+    """Far into the negative tail, too. Roundings counted for Phi: 2.2 * 2^-24 of the fit; 16 of
+    the polynomial and its argument; z^2 / 2 in the exponent with 6 * 2^-24 of its own size (x,
+    its square, the constants), which the exponential turns into as much of the value; 8 of the
+    exponential and the products."""
+    v = torch.linspace(-12, 12, 505, device="cuda").to(torch.bfloat16)
+    z = v.double()
+    ref = 0.5 * z * torch.special.erfc(-z * math.sqrt(0.5))  # ndtr is 0 below -8.3
+    rel = (32 + 3 * z * z) * F32
+    for f32 in (False, True):
+        y = act_of_values(skg, v, "gelu", M, K, mode, f32)
+        assert ((y - ref).abs() <= ref.abs() * (rel + (F32 if f32 else BF16 * (1 + rel)))).all()
