@@ -37,6 +37,7 @@ import functools
 import os
 
 import torch
+from torch.overrides import TorchFunctionMode
 
 from . import _on_device, _stream_handle, lib, skinny_gemm_bf16
 from . import linear as _linear_call
@@ -287,24 +288,51 @@ def _norm_forward(self, x):
     return type(self).forward(self, x)
 
 
+class _RoutedProduct(TorchFunctionMode):
+    """Within it, F.linear on the given weight, as nn.Linear.forward calls it, is routed."""
+
+    def __init__(self, weight, fallback):
+        super().__init__()
+        self.weight, self.fallback = weight, fallback
+
+    def __torch_function__(self, func, types, args=(), kwargs=None):
+        if func is torch.nn.functional.linear and len(args) == 3 and args[1] is self.weight:
+            return skinny_linear(*args, fallback=self.fallback)
+        return func(*args, **(kwargs or {}))
+
+
+def _linear_forward(self, inp, fallback):
+    """nn.Linear.forward, routed."""
+    if getattr(self, "_skinny_fused", False) and self.bias is not None and qualifies_fused(inp, self.weight, self.bias):
+        return linear_act(inp, self.weight, self.bias, None, "none", False)
+    return skinny_linear(inp, self.weight, self.bias, fallback=fallback)
+
+
+def _own_linear_forward(self, *args, _skinny_fallback, **kwargs):
+    """The forward of a class derived from nn.Linear, with its weight's product routed."""
+    with _RoutedProduct(self.weight, _skinny_fallback):
+        return type(self).forward(self, *args, **kwargs)
+
+
 def install(module: torch.nn.Module, fallback: bool = True, fused: bool = False) -> int:
     """Route the forward of every nn.Linear inside ``module`` through
-    :func:`skinny_linear`. With ``fused``, layers with a bias and up to 64 rows of input
-    run on linear_act and nn.RMSNorm modules on rms_norm, both where no gradient is asked
-    for; classes with a forward of their own keep it, and layers that an earlier call
-    hooked without ``fused`` take it up. Returns the number of modules hooked."""
+    :func:`skinny_linear`. A class derived from it that has a forward of its own keeps that:
+    what it does with the product stays, and the product by its weight is routed where it
+    calls nn.Linear's forward or F.linear for it. With ``fused``, nn.Linear layers with a
+    bias and up to 64 rows of input run on linear_act and nn.RMSNorm modules on rms_norm,
+    both where no gradient is asked for; classes with a forward of their own do not, and
+    layers that an earlier call hooked without ``fused`` take it up. Returns the number of
+    modules hooked."""
     count = 0
     for sub in module.modules():
         if fused and type(sub).forward is torch.nn.Linear.forward:
             sub._skinny_fused = True
         if getattr(sub, "_skinny_hooked", False):
             continue
-        if isinstance(sub, torch.nn.Linear):
-            def fwd(self, inp, _fallback=fallback):
-                if getattr(self, "_skinny_fused", False) and self.bias is not None and qualifies_fused(inp, self.weight, self.bias):
-                    return linear_act(inp, self.weight, self.bias, None, "none", False)
-                return skinny_linear(inp, self.weight, self.bias, fallback=_fallback)
-            sub.forward = functools.partial(fwd, sub)
+        if type(sub).forward is torch.nn.Linear.forward:
+            sub.forward = functools.partial(_linear_forward, sub, fallback=fallback)
+        elif isinstance(sub, torch.nn.Linear):
+            sub.forward = functools.partial(_own_linear_forward, sub, _skinny_fallback=fallback)
         elif fused and type(sub).forward is torch.nn.RMSNorm.forward:
             sub.forward = functools.partial(_norm_forward, sub)
         else:

@@ -1,0 +1,112 @@
+"""What install() leaves as it was: classes with a forward of their own, and calls that ask
+for derivatives. On the CPU every product takes the standard path, so the results of a hooked
+module are those of the module before, and the routing is seen by its calls."""
+from __future__ import annotations
+
+import copy
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def op():
+    from bf16_skinny_gemm_amd import torch_op
+
+    return torch_op
+
+
+class Doubled(torch.nn.Linear):
+    def forward(self, x):
+        return 2 * super().forward(x)
+
+
+class Adapted(torch.nn.Linear):
+    """A low-rank update beside the product, and an argument that nn.Linear does not have."""
+
+    def __init__(self, *args, **kwargs):
+        super().__init__(*args, **kwargs)
+        self.down = torch.nn.Parameter(torch.randn(4, self.in_features))
+        self.up = torch.nn.Parameter(torch.randn(self.out_features, 4))
+
+    def forward(self, x, *, update=True):
+        y = torch.nn.functional.linear(x, self.weight, self.bias)
+        return y + (x @ self.down.t()) @ self.up.t() if update else y
+
+
+class Masked(torch.nn.Linear):
+    """A product with another matrix than the weight."""
+
+    def forward(self, x):
+        return torch.nn.functional.linear(x, self.weight.tril(), self.bias)
+
+
+class Renamed(torch.nn.Linear):
+    """No forward of its own."""
+
+
+@pytest.mark.parametrize("fused", [False, True])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("cls", [Doubled, Adapted, Masked, Renamed])
+def test_a_linear_class_keeps_its_own_forward(op, cls, bias, fused):
+    torch.manual_seed(0)
+    layer = cls(24, 16, bias=bias)
+    x = torch.randn(3, 24)
+    want = layer(x)
+    model = torch.nn.Sequential(layer)
+    assert op.install(model, fused=fused) == 1 and op.install(model, fused=fused) == 0
+    assert torch.equal(layer(x), want)
+    assert torch.equal(copy.deepcopy(model)(x), want)
+    if cls is Adapted:
+        assert torch.equal(layer(x, update=False), torch.nn.functional.linear(x, layer.weight, layer.bias))
+    layer(x).sum().backward()
+    assert layer.weight.grad is not None
+
+
+@pytest.mark.parametrize("cls,calls", [(Doubled, 1), (Adapted, 1), (Masked, 0), (Renamed, 1)])
+def test_the_product_by_the_weight_is_routed(op, monkeypatch, cls, calls):
+    seen = []
+    plain = op.skinny_linear
+
+    def routed(x, weight, bias=None, fallback=True):
+        seen.append((weight, fallback))
+        return plain(x, weight, bias, fallback)
+
+    monkeypatch.setattr(op, "skinny_linear", routed)
+    layer = cls(8, 8, bias=False)
+    op.install(torch.nn.Sequential(layer), fallback=True)
+    layer(torch.randn(2, 8))
+    assert len(seen) == calls and all(w is layer.weight and f for w, f in seen)
+    torch.nn.functional.linear(torch.randn(2, 8), layer.weight)  # outside of the layer
+    assert len(seen) == calls
+
+
+def test_own_forward_without_fallback_refuses_what_does_not_qualify(op):
+    layer = Doubled(8, 8, bias=False)
+    op.install(torch.nn.Sequential(layer), fallback=False)
+    with pytest.raises(ValueError):
+        layer(torch.randn(2, 8))
+
+
+def test_own_forward_compiles(op):
+    torch.manual_seed(0)
+    model = torch.nn.Sequential(Doubled(8, 8, bias=False), torch.nn.Linear(8, 8))
+    x = torch.randn(2, 8)
+    want = model(x)
+    op.install(model)
+    with torch.no_grad():
+        assert torch.equal(torch.compile(model, backend="aot_eager")(x), want)
+
+
+@pytest.mark.gpu
+def test_own_forward_on_the_kernels(op):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.manual_seed(0)
+    layer = Doubled(256, 128, bias=False).cuda().to(torch.bfloat16)
+    many, few = (torch.randn(m, 256, device="cuda").to(torch.bfloat16) for m in (20, 4))
+    want = layer(many)
+    assert op.install(torch.nn.Sequential(layer), fused=True) == 1
+    with torch.no_grad():
+        assert torch.equal(layer(many), want)
+        assert torch.equal(layer(few), 2 * op.linear(few, layer.weight))
