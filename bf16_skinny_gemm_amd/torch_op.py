@@ -37,6 +37,7 @@ import functools
 import os
 
 import torch
+from torch.autograd import forward_ad
 from torch.overrides import TorchFunctionMode
 
 from . import _on_device, _stream_handle, lib, skinny_gemm_bf16
@@ -243,11 +244,24 @@ linear_fp8 = torch.ops.skinny.linear_fp8.default
 linear_gated_fp8 = torch.ops.skinny.linear_gated_fp8.default
 
 
+_func_level = torch._C._functorch.maybe_current_level
+
+
+def _transformed(*tensors) -> bool:
+    """A torch.func transform is at work, or a tensor carries a forward-mode tangent: the
+    operators have rules for neither and would drop the derivative."""
+    if _func_level() is not None:
+        return True
+    return forward_ad._current_level >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def skinny_linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
                   fallback: bool = True) -> torch.Tensor:
     """F.linear semantics, routed: the skinny GEMM when the call qualifies,
-    otherwise torch.nn.functional.linear if ``fallback`` (else ValueError)."""
-    if qualifies(x, weight, bias):
+    otherwise torch.nn.functional.linear if ``fallback`` (else ValueError). Calls inside a
+    torch.func transform or with forward-mode tangents do not qualify."""
+    if qualifies(x, weight, bias) and not _transformed(x, weight):
         return torch.ops.skinny.linear(x, weight)
     if not fallback:
         raise ValueError("skinny_linear: call does not qualify for the skinny GEMM")
@@ -260,8 +274,9 @@ FUSED_ROWS = 64
 
 
 def _inference(*tensors) -> bool:
-    """No gradient is asked for: the operators record none."""
-    return not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors))
+    """No derivative is asked for: the operators record none."""
+    return not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)) and (
+        not _transformed(*tensors))
 
 
 def qualifies_fused(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None) -> bool:
@@ -320,7 +335,7 @@ def install(module: torch.nn.Module, fallback: bool = True, fused: bool = False)
     what it does with the product stays, and the product by its weight is routed where it
     calls nn.Linear's forward or F.linear for it. With ``fused``, nn.Linear layers with a
     bias and up to 64 rows of input run on linear_act and nn.RMSNorm modules on rms_norm,
-    both where no gradient is asked for; classes with a forward of their own do not, and
+    both where no derivative is asked for; classes with a forward of their own do not, and
     layers that an earlier call hooked without ``fused`` take it up. Returns the number of
     modules hooked."""
     count = 0

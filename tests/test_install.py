@@ -110,3 +110,79 @@ def test_own_forward_on_the_kernels(op):
     with torch.no_grad():
         assert torch.equal(layer(many), want)
         assert torch.equal(layer(few), 2 * op.linear(few, layer.weight))
+
+
+def derivatives(model, x, t):
+    """The model's directional derivative, three ways."""
+    import torch.autograd.forward_ad as fw
+
+    with fw.dual_level():
+        got = [fw.unpack_dual(model(fw.make_dual(x, t))).tangent]
+    got.append(torch.func.jvp(model, (x,), (t,))[1])
+    params = {k: v.detach() for k, v in model.named_parameters()}
+    along = {k: torch.ones_like(v) for k, v in params.items()}
+    got.append(torch.func.jvp(lambda p: torch.func.functional_call(model, p, (x,)), (params,), (along,))[1])
+    return got
+
+
+def test_derivatives_do_not_reach_the_operators(op, monkeypatch):
+    """With every call taken for one that qualifies, those with a tangent or inside a transform
+    still run on the standard path (the operator itself refuses CPU tensors)."""
+    import torch.autograd.forward_ad as fw
+
+    torch.manual_seed(0)
+    model = torch.nn.Sequential(torch.nn.Linear(8, 8, bias=False), torch.nn.Tanh())
+    x, t = torch.randn(2, 8), torch.randn(2, 8)
+    want = derivatives(model, x, t)
+    each = torch.vmap(model)(x)
+    op.install(model)
+    monkeypatch.setattr(op, "qualifies", lambda *args: True)
+    with pytest.raises(ValueError, match="skinny::linear"):
+        model(x)
+    for a, b in zip(derivatives(model, x, t), want):
+        assert torch.equal(a, b)
+    assert torch.equal(torch.vmap(model)(x), each)
+    model[0].forward.keywords["fallback"] = False
+    with pytest.raises(ValueError, match="qualify"):
+        torch.func.jvp(model, (x,), (t,))
+    # the condition of the operators that fused takes
+    seen = []
+    torch.func.jvp(lambda a: (seen.append(op._inference(a, None)), a)[1], (x,), (t,))
+    with fw.dual_level(), torch.no_grad():
+        seen += [op._inference(None, fw.make_dual(x, t)), op._inference(x, None)]
+    assert seen == [False, False, True] and op._inference(x)
+
+
+@pytest.mark.gpu
+def test_derivatives_through_a_fused_model(op):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.manual_seed(0)
+    # apart: torch's own norm gives float32 under a tangent, which the next layer refuses
+    models = [torch.nn.Sequential(m).cuda().to(torch.bfloat16).requires_grad_(False)
+              for m in (torch.nn.RMSNorm(64), torch.nn.Linear(64, 32), torch.nn.Linear(64, 16, bias=False))]
+    x, t = (torch.randn(4, 64, device="cuda").to(torch.bfloat16) for _ in range(2))
+    for model in models:
+        want = derivatives(model, x, t)
+        assert all(bool(w.any()) for w in want)
+        assert op.install(model, fused=True) == 1
+        for a, b in zip(derivatives(model, x, t), want):
+            assert torch.equal(a, b)
+    (norm,), (lin,), (bare,) = models
+    assert torch.equal(norm(x), op.rms_norm(x, norm.weight, torch.finfo(torch.float32).eps))
+    assert torch.equal(lin(x), op.linear_act(x, lin.weight, lin.bias))
+    assert torch.equal(bare(x), op.linear(x, bare.weight))
+
+
+@pytest.mark.gpu
+def test_a_fused_model_compiles(op):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.manual_seed(0)
+    model = torch.nn.Sequential(torch.nn.RMSNorm(64), torch.nn.Linear(64, 32), Doubled(32, 16, bias=False))
+    model = model.cuda().to(torch.bfloat16)
+    x = torch.randn(4, 64, device="cuda").to(torch.bfloat16)
+    op.install(model, fused=True)
+    with torch.no_grad():
+        want = model(x)
+        assert torch.equal(torch.compile(model, backend="aot_eager", fullgraph=True)(x), want)
