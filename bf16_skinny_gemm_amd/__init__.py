@@ -565,6 +565,8 @@ def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device
         raise ValueError(f"{name} must be on {device or 'a GPU'}, got {t.device}")
     if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
         raise ValueError(f"{name} must be {list(shape) if shape else '2-D'}, got {list(t.shape)}")
+    if max(t.shape) > 0x7FFFFFFF:  # the argument structures would cut them off
+        raise ValueError(f"{name}'s sizes must fit in 31 bits, got {list(t.shape)}")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride, got stride {t.stride()}")
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]

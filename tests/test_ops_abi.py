@@ -194,3 +194,18 @@ def test_operators_give_shapes_to_a_tracer(skg):
     assert t.linear_gated_fp8(q, s, wq, ws, wq, ws).shape == (2, 3, 40)
     with pytest.raises(ValueError):
         t.rms_norm_fp8(x, n, 1e-6, 64)
+
+
+def test_python_helpers_refuse_sizes_past_31_bits(skg):
+    """The argument structures hold 32 bits and would cut them off without a word (tensors
+    without memory: the sizes are refused before an address is asked for)."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    bf, big = torch.bfloat16, 2 ** 32 + 5
+    with FakeTensorMode():
+        one, tall, wide = (torch.empty(*s, dtype=bf, device="cuda") for s in ((1,), (big, 1), (1, big)))
+        for call in (lambda: skg.rms_norm(tall, one), lambda: skg.rms_norm(wide, wide[0]),
+                     lambda: skg.linear(tall, one[None]), lambda: skg.linear(one[None], tall),
+                     lambda: skg.linear(wide, wide)):
+            with pytest.raises(ValueError, match="31 bits"):
+                call()
