@@ -288,6 +288,8 @@ def qualifies_fused(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | 
             return False
     if x.shape[-1] != weight.shape[1] or x.numel() // x.shape[-1] > FUSED_ROWS:
         return False
+    if torch.is_autocast_enabled("cuda") and torch.get_autocast_dtype("cuda") != torch.bfloat16:
+        return False  # F.linear would compute in, and return, that type
     return _inference(x, weight, bias) and _device_is_gfx950(x.device)
 
 

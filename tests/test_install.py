@@ -186,3 +186,22 @@ def test_a_fused_model_compiles(op):
     with torch.no_grad():
         want = model(x)
         assert torch.equal(torch.compile(model, backend="aot_eager", fullgraph=True)(x), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_fused_under_autocast(op, dtype):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.manual_seed(0)
+    model = torch.nn.Sequential(torch.nn.RMSNorm(64), torch.nn.Linear(64, 32)).cuda().to(torch.bfloat16)
+    x = torch.randn(4, 64, device="cuda").to(torch.bfloat16)
+    with torch.no_grad(), torch.autocast("cuda", dtype=dtype):
+        norm, want = model[0](x), model(x)
+        op.install(model, fused=True)
+        assert model[0](x).dtype == norm.dtype and model(x).dtype == want.dtype == dtype
+        y = model[0](x)
+        if dtype == torch.bfloat16:
+            assert torch.equal(model[1](y), op.linear_act(y, model[1].weight, model[1].bias))
+        else:
+            assert torch.equal(model[1](y), torch.nn.functional.linear(y, model[1].weight, model[1].bias))
