@@ -17,7 +17,8 @@ Python ints; a non-zero status raises :class:`SkinnyError`):
     skinny_gemm_split_k_workspace_bytes, skinny_gemm_bf16_split_k,
     skinny_gemm_bf16_split_k_noalloc, skinny_gemm_split_k_num_variants,
     skinny_gemm_split_k_get_variant, skinny_gemm_split_k_default_plan,
-    skinny_rms_norm_bf16, skinny_rms_norm_fp8, skinny_linear_bf16, skinny_linear_fp8
+    skinny_rms_norm_bf16, skinny_rms_norm_fp8, skinny_linear_bf16, skinny_linear_fp8,
+    skinny_linear_default_plan
 
 Tensor helpers: :func:`gemm`, :func:`gemm_pair`, :func:`gemm_pair_strided`,
 :func:`split_k_workspace`, :func:`gemm_split_k` and :func:`gemm_split_k_noalloc`;
@@ -55,6 +56,10 @@ SKINNY_ACT_SILU = 4
 
 SKINNY_SCALES_ROW = 1
 SKINNY_SCALES_BLOCK = 2
+
+SKINNY_LINEAR_ELEMENTS = 0
+SKINNY_LINEAR_STREAM = 1
+SKINNY_LINEAR_TILE = 2
 
 ACTS = {"none": SKINNY_ACT_NONE, "relu": SKINNY_ACT_RELU, "gelu": SKINNY_ACT_GELU,
         "gelu_tanh": SKINNY_ACT_GELU_TANH, "silu": SKINNY_ACT_SILU}
@@ -119,6 +124,18 @@ class LinearArgs(ctypes.Structure):
     ]
 
 
+class LinearPlan(ctypes.Structure):
+    """skinny_linear_plan_t."""
+
+    _fields_ = [(name, ctypes.c_int32) for name in ("kind", "features", "rows", "waves", "ring", "index", "count")]
+
+    def as_dict(self) -> dict:
+        return {f[0]: int(getattr(self, f[0])) for f in self._fields_}
+
+    def __repr__(self):
+        return "LinearPlan(" + ", ".join(f"{k}={v}" for k, v in self.as_dict().items()) + ")"
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -162,6 +179,9 @@ def lib() -> ctypes.CDLL:
                            ("skinny_linear_bf16", LinearArgs), ("skinny_linear_fp8", LinearArgs)):
             getattr(L, name).argtypes = [ctypes.POINTER(args), vp]
             getattr(L, name).restype = ctypes.c_int
+        L.skinny_linear_default_plan.argtypes = [ctypes.POINTER(LinearArgs), ctypes.c_int32,
+                                                 ctypes.POINTER(LinearPlan)]
+        L.skinny_linear_default_plan.restype = ctypes.c_int
         for name in ("skinny_gemm_init", "skinny_gemm_bf16", "skinny_gemm_bf16_pair",
                      "skinny_gemm_bf16_ex", "skinny_gemm_bf16_pair_ex", "skinny_gemm_bf16_f32out",
                      "skinny_gemm_bf16_f32out_ex", "skinny_gemm_bf16_pair_strided",
@@ -325,6 +345,13 @@ def skinny_linear_bf16(args: LinearArgs, stream: int = 0) -> None:
 
 def skinny_linear_fp8(args: LinearArgs, stream: int = 0) -> None:
     _check(lib().skinny_linear_fp8(ctypes.byref(args), stream), "skinny_linear_fp8")
+
+
+def skinny_linear_default_plan(args: LinearArgs, compute_units: int = 256) -> LinearPlan:
+    p = LinearPlan()
+    _check(lib().skinny_linear_default_plan(ctypes.byref(args), compute_units, ctypes.byref(p)),
+           "skinny_linear_default_plan")
+    return p
 
 
 # ---- tensor helpers ---------------------------------------------------------
@@ -713,8 +740,9 @@ __all__ = [
     "skinny_gemm_get_variant", "skinny_gemm_status_string", "skinny_gemm_version",
     "SKINNY_OK", "SKINNY_ERR_INVALID_ARG", "SKINNY_ERR_UNSUPPORTED", "SKINNY_ERR_NOT_INITIALIZED",
     "SKINNY_ERR_LAUNCH", "SKINNY_KIND_FIXED_K", "SKINNY_KIND_LOOP_K", "SKINNY_KIND_SCALAR",
-    "SKINNY_KIND_MFMA", "NormArgs", "LinearArgs", "ACTS", "rms_norm", "linear",
+    "SKINNY_KIND_MFMA", "NormArgs", "LinearArgs", "LinearPlan", "ACTS", "rms_norm", "linear",
     "skinny_rms_norm_bf16", "skinny_rms_norm_fp8", "skinny_linear_bf16", "skinny_linear_fp8",
+    "skinny_linear_default_plan", "SKINNY_LINEAR_ELEMENTS", "SKINNY_LINEAR_STREAM", "SKINNY_LINEAR_TILE",
     "SKINNY_ACT_NONE", "SKINNY_ACT_RELU", "SKINNY_ACT_GELU", "SKINNY_ACT_GELU_TANH",
     "SKINNY_ACT_SILU", "SKINNY_SCALES_ROW", "SKINNY_SCALES_BLOCK",
 ]

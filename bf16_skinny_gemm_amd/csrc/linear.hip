@@ -94,6 +94,7 @@ struct Choice {
     const void *fn;
     int64_t nt, mt;  // blocks along N and M
     int waves;
+    skinny_linear_plan_t plan;
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -128,7 +129,8 @@ Choice choose(int mode, bool gated, bool exact, int M, int N, int64_t kbytes, in
                                : stream_kernels_block(M, gated, exact, s);
     for (int i = 0; i < ns; ++i) {
         const StreamKernel &k = s[i];
-        const Choice c{k.fn, ceil_div(N, k.nb), ceil_div(M, k.bm), k.waves};
+        const Choice c{k.fn, ceil_div(N, k.nb), ceil_div(M, k.bm), k.waves,
+                       {SKINNY_LINEAR_STREAM, k.nb, k.bm, k.waves, k.ring, i, 0}};
         const double per_cu = (double)ceil_div(c.nt * c.mt, cus);
         double at_once = 163840 / k.lds < 32 / k.waves ? 163840 / k.lds : 32 / k.waves;
         const double turns = std::ceil((double)(c.nt * c.mt) / (cus * at_once));
@@ -140,6 +142,7 @@ Choice choose(int mode, bool gated, bool exact, int M, int N, int64_t kbytes, in
         most = most > trips ? most : trips;
         offer(c, 3.0 + most + 0.2 * (hbm + lds + trips) + turns * (0.344 + 0.0292 * k.waves * k.tiles));
     }
+    best.plan.count = ns;
     if (M <= 16)  // W once: a tile of many rows only adds work
         return best;
     TileKernel t[kTileMost];
@@ -148,11 +151,24 @@ Choice choose(int mode, bool gated, bool exact, int M, int N, int64_t kbytes, in
                                 : tile_kernels_block(gated, exact, t);
     for (int i = 0; i < ntk; ++i) {
         const TileKernel &k = t[i];
-        const Choice c{k.fn, ceil_div(N, k.nb), ceil_div(M, k.bm), k.waves};
+        const Choice c{k.fn, ceil_div(N, k.nb), ceil_div(M, k.bm), k.waves,
+                       {SKINNY_LINEAR_TILE, k.nb, k.bm, k.waves, 0, ns + i, 0}};
         const double per_cu = (double)ceil_div(c.nt * c.mt, cus);
         offer(c, 5.5 + per_cu * (0.5 + stages * k.stage_us) + out);
     }
+    best.plan.count = ns + ntk;
     return best;
+}
+
+// The kernel of a checked call with outputs; fn is null for the element-wise one.
+Choice plan_of(const skinny_linear_t &p, bool fp8, int cus)
+{
+    Choice c{};
+    if (linear_vector_ok(p, fp8))
+        c = choose(p.scales, p.W1 != nullptr, p.out_f32 != 0, p.M, p.N, (int64_t)p.K * (fp8 ? 1 : 2), cus);
+    if (!c.fn || c.nt * c.mt > kMaxBlocks)
+        c = Choice{nullptr, 0, 0, 4, {SKINNY_LINEAR_ELEMENTS, 16, 16, 4, 0, -1, 0}};
+    return c;
 }
 
 int run_linear(const skinny_linear_t *p, bool fp8, hipStream_t stream)
@@ -187,19 +203,14 @@ int run_linear(const skinny_linear_t *p, bool fp8, hipStream_t stream)
     a.act = p->act;
     a.out_f32 = p->out_f32;
 
-    // the element-wise kernel loops over its tiles, so it takes any size
-    auto launch_any = [&]() {
+    const Choice c = plan_of(*p, fp8, cus);
+    if (!c.fn) {  // the element-wise kernel loops over its tiles, so it takes any size
         int nt = (int)(((int64_t)a.N + 15) / 16);
         int64_t tiles = (((int64_t)a.M + 15) / 16) * nt;
         void *args[] = {&a, &tiles, &nt};
         return ops_launch(any_fn(mode, gated), dim3((unsigned)(tiles < (1 << 20) ? tiles : 1 << 20)), 256, args,
                           stream);
-    };
-    if (!linear_vector_ok(*p, fp8))
-        return launch_any();
-    const Choice c = choose(mode, gated, a.out_f32 != 0, a.M, a.N, (int64_t)a.K * (fp8 ? 1 : 2), cus);
-    if (c.nt * c.mt > kMaxBlocks)
-        return launch_any();
+    }
     int nt = (int)c.nt, mt = (int)c.mt;
     void *args[] = {&a, &nt, &mt};
     return ops_launch(c.fn, dim3((unsigned)(c.nt * c.mt)), c.waves * 64, args, stream);
@@ -218,6 +229,20 @@ int skinny_linear_bf16(const skinny_linear_t *args, hipStream_t stream)
 int skinny_linear_fp8(const skinny_linear_t *args, hipStream_t stream)
 {
     return skg_host::run_linear(args, true, stream);
+}
+
+int skinny_linear_default_plan(const skinny_linear_t *args, int32_t compute_units, skinny_linear_plan_t *out)
+{
+    if (!args || !out || compute_units < 1)
+        return SKINNY_ERR_INVALID_ARG;
+    const bool fp8 = args->scales != 0;
+    const int st = skg_host::validate_linear(args, fp8);
+    if (st != SKINNY_OK)
+        return st;
+    if (args->M == 0 || args->N == 0)
+        return SKINNY_ERR_INVALID_ARG;
+    *out = skg_host::plan_of(*args, fp8, compute_units).plan;
+    return SKINNY_OK;
 }
 
 }  // extern "C"

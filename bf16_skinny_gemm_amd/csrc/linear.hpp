@@ -328,7 +328,7 @@ struct TileKernel {
     int nb, bm, waves;
     float stage_us;
 };
-constexpr int kTileMost = 5;
+constexpr int kTileMost = 4;
 
 // The kernels that take M rows, by element type and scales; returns their number.
 int stream_kernels_bf16(int M, bool gated, bool exact, StreamKernel *out);

@@ -120,6 +120,29 @@ int skinny_linear_bf16(const skinny_linear_t *args, hipStream_t stream);
  * of the largest: about 2e-5 of a result's norm, below bfloat16's rounding of 4e-3. */
 int skinny_linear_fp8(const skinny_linear_t *args, hipStream_t stream);
 
+/* The kernel that a projection call takes. Calls with the same element type, scales, gate,
+ * output type and class of rows (up to 8, up to 16, more) choose among the same `count`
+ * kernels, numbered by `index`. */
+typedef enum skinny_linear_kind {
+    SKINNY_LINEAR_ELEMENTS = 0, /* one output per thread: what is not 16-byte aligned */
+    SKINNY_LINEAR_STREAM = 1,   /* K split over the waves of a block */
+    SKINNY_LINEAR_TILE = 2      /* LDS tiles shared by the waves of a block */
+} skinny_linear_kind_t;
+
+typedef struct skinny_linear_plan {
+    int32_t kind;               /* skinny_linear_kind_t */
+    int32_t features, rows;     /* outputs of a block */
+    int32_t waves;              /* of a block */
+    int32_t ring;               /* stages of K that a wave holds (SKINNY_LINEAR_STREAM) */
+    int32_t index, count;       /* -1 and 0 for SKINNY_LINEAR_ELEMENTS */
+} skinny_linear_plan_t;
+
+/* The plan of skinny_linear_bf16(args) (scales 0) or skinny_linear_fp8(args) (else) on a
+ * device with that many compute units (256: a whole MI355X). Checks args as the call does,
+ * touches no device and follows no pointer. SKINNY_ERR_INVALID_ARG for a call without
+ * outputs. */
+int skinny_linear_default_plan(const skinny_linear_t *args, int32_t compute_units, skinny_linear_plan_t *out);
+
 #ifdef __cplusplus
 }
 #endif
