@@ -34,6 +34,7 @@ refused launch raises.
 from __future__ import annotations
 
 import functools
+import math
 import os
 
 import torch
@@ -171,11 +172,11 @@ def _norm_py(x, weight, eps, residual=None, quant=None):
 def _linear_py(x, weight, bias, residual, act, out_f32, W_up=None, bias_up=None, x_scale=None,
                w_scale=None, w_up_scale=None):
     """Python kernels of the projections (used when the C++ operators are not built)."""
-    K, N = x.shape[-1], weight.shape[0]
+    K, N, M = x.shape[-1], weight.shape[0], math.prod(x.shape[:-1])
     if x_scale is not None:
-        x_scale = x_scale.reshape(-1) if w_scale.dim() == 1 else x_scale.reshape(-1, x_scale.shape[-1])
-    y = _linear_call(x.reshape(-1, K), weight, bias=bias, act=act, W_up=W_up, bias_up=bias_up,
-                     residual=None if residual is None else residual.reshape(-1, N),
+        x_scale = x_scale.reshape(M) if w_scale.dim() == 1 else x_scale.reshape(M, x_scale.shape[-1])
+    y = _linear_call(x.reshape(M, K), weight, bias=bias, act=act, W_up=W_up, bias_up=bias_up,
+                     residual=None if residual is None else residual.reshape(M, N),
                      x_scale=x_scale, w_scale=w_scale, w_up_scale=w_up_scale,
                      out_dtype=torch.float32 if out_f32 else torch.bfloat16)
     return y.reshape(*x.shape[:-1], N)

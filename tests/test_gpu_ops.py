@@ -731,3 +731,23 @@ def test_gelu_is_right_relative_to_its_value(skg, M, K, mode):
     for f32 in (False, True):
         y = act_of_values(skg, v, "gelu", M, K, mode, f32)
         assert ((y - ref).abs() <= ref.abs() * (rel + (F32 if f32 else BF16 * (1 + rel)))).all()
+
+
+@pytest.mark.parametrize("shape,N", [((2, 3, 0), 40), ((5, 0), 40), ((0, 3, 64), 40), ((4, 64), 0), ((0, 0), 40)])
+def test_python_kernels_agree_on_empty_sizes(ops, shape, N):
+    g, bf, K = gen(12), torch.bfloat16, shape[-1]
+    x = torch.randn(*shape, generator=g, device="cuda").to(bf)
+    w, b = torch.randn(N, K, generator=g, device="cuda").to(bf), torch.randn(N, generator=g, device="cuda").to(bf)
+    r = torch.randn(*shape[:-1], N, generator=g, device="cuda").to(bf)
+    e4 = torch.float8_e4m3fn
+    kb, nb = -(-K // 128), -(-N // 128)
+    rows = (torch.ones(shape[:-1], device="cuda"), torch.ones(N, device="cuda"))
+    blocks = (torch.ones(*shape[:-1], kb, device="cuda"), torch.ones(nb, kb, device="cuda"))
+    calls = [("linear_act", (x, w, b, r, "silu", True))]
+    calls += [("linear_fp8", (x.to(e4), xs, w.to(e4), ws, b, r, "silu", True)) for xs, ws in (rows, blocks)]
+    for name, args in calls:
+        want, got = getattr(ops, name)(*args), ops._PY_KERNELS[name](*args)
+        assert want.shape == got.shape == (*shape[:-1], N) and torch.equal(bits(want), bits(got))
+        if K == 0:
+            ref = act_ref(b.double(), "silu") + r.double()
+            assert ((want.double() - ref).abs() <= 32 * F32 * (ref.abs() + b.double().abs())).all()
