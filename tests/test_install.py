@@ -205,3 +205,40 @@ def test_fused_under_autocast(op, dtype):
             assert torch.equal(model[1](y), op.linear_act(y, model[1].weight, model[1].bias))
         else:
             assert torch.equal(model[1](y), torch.nn.functional.linear(y, model[1].weight, model[1].bias))
+
+
+def test_fused_takes_layers_whose_rows_are_whole_pieces(op, monkeypatch):
+    """Rows that do not start at multiples of 16 bytes would run element-wise."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    monkeypatch.setattr(op, "_device_is_gfx950", lambda device: True)
+    with FakeTensorMode():
+        def make(*shape):
+            return torch.empty(*shape, dtype=torch.bfloat16, device="cuda")
+
+        def takes(x, w):
+            return op.qualifies_fused(x, w, make(w.shape[0]))
+
+        w = make(32, 64)
+        for x in (make(4, 64), make(64), make(2, 3, 64), make(2, 3, 64).transpose(0, 1), make(4, 72)[:, :64],
+                  make(4, 80)[:, 8:72], make(64, 4).t(), make(5, 64)[1:]):
+            assert takes(x, w)
+        for x in (make(4, 65)[:, :64], make(4, 72)[:, 4:68], make(4 * 64 + 1)[1:].view(4, 64),
+                  make(6 * 64 + 4)[4:].view(2, 3, 64), make(65, 64)):
+            assert not takes(x, w)
+        assert not takes(make(4, 60), make(32, 60)) and not takes(make(4, 1001), make(32, 1001))
+        assert not takes(make(4, 64), make(32 * 64 + 1)[1:].view(32, 64))
+
+
+@pytest.mark.gpu
+def test_fused_leaves_odd_widths_to_the_standard_path(op):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    layer = torch.nn.Linear(1001, 64).cuda().to(torch.bfloat16)
+    x = torch.randn(4, 1001, device="cuda").to(torch.bfloat16)
+    with torch.no_grad():
+        want = layer(x)
+        op.install(torch.nn.Sequential(layer), fused=True)
+        assert torch.equal(layer(x), want)
+        y = layer(torch.randn(4, 1008, device="cuda").to(torch.bfloat16)[:, :1001])
+        assert y.shape == (4, 64)
