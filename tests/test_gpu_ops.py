@@ -751,3 +751,16 @@ def test_python_kernels_agree_on_empty_sizes(ops, shape, N):
         if K == 0:
             ref = act_ref(b.double(), "silu") + r.double()
             assert ((want.double() - ref).abs() <= 32 * F32 * (ref.abs() + b.double().abs())).all()
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("M,N,K", [(700, 1031, 8208), (2100, 1100, 4112), (260, 8200, 5136)])
+def test_linear_deep_tiles(skg, M, N, K, mode):
+    """Many stages of the tiled kernels; the block scales of neighbouring stages differ."""
+    check_linear(skg, M, N, K, mode, bias=True, residual=True, seed=K)
+    check_linear(skg, M, N // 2, K, mode, gated=True, act="silu", seed=K)
+    x, w, xs, ws, _, _ = make_linear(M, N, K, mode, 1, K + 1)
+    kw = dict(x_scale=xs, w_scale=ws[0] if ws else None)
+    first = skg.linear(x, w[0], **kw)
+    for _ in range(5):
+        assert torch.equal(bits(skg.linear(x, w[0], **kw)), bits(first))
