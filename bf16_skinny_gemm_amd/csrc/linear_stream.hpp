@@ -8,10 +8,10 @@
 // loads only, while the loads of its later stages and of the other waves are in flight.
 // The loads write LDS directly, 8 rows of 128 bytes an instruction: a compute unit takes
 // 64 bytes a clock that way, against 16 where an instruction loads 16 rows of 64 bytes,
-// as the operand registers of the matrix instructions want them. Bound by HBM (few rows:
-// 1 x 4096 x 4096 bfloat16 5.1 us, 6.6 TB/s; 1 x 12576 x 4096 e4m3 8.0 us, 6.5 TB/s) or by
-// the 64 bytes a clock of W and x (many: 100 x 4096 x 8192 e4m3 12.6 us, 62 KB/us a compute
-// unit over the whole launch).
+// as the operand registers of the matrix instructions want them. Bound by HBM (few rows,
+// medians of cold launches: 1 x 4096 x 4096 bfloat16 6.2 us, 5.5 TB/s; 1 x 12576 x 4096 e4m3
+// 9.1 us, 5.6 TB/s) or by the 64 bytes a clock of W and x (many: 100 x 4096 x 8192 e4m3
+// 13.5 us, 58 KB/us a compute unit over the whole launch).
 #pragma once
 
 #include "lds_load.hpp"

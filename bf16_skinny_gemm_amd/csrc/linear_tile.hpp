@@ -26,10 +26,15 @@
 // the two register files at every step): stages past the last read zeros, since every
 // load past K does, and add nothing.
 //
-// Bound by the matrix pipe and its power limit: 4096^3 in bfloat16 95 to 110 us by the card
-// (1250 to 1450 TF), 106 to 110 with residual, activation and cold inputs; e4m3 with row
-// scales 4096 x 4096 x 8192 in 98 to 103 (2670 to 2800 TF). At the tiles of 128 x 128, by what a compute unit takes into LDS (32 KB a stage at
-// some 75 KB/us).
+// Bound by the matrix pipe at the clock that it leaves (1.75 GHz of 2.4 while products of
+// 4096 rows run one after another): 4096^3 in bfloat16 96 to 105 us by the card (1310 to
+// 1430 TF), 107 to 118 with residual, activation and cold inputs; e4m3 with row scales
+// 4096 x 4096 x 8192 in 92 to 97 (2830 to 2990 TF), 101 to 108 with bias, residual and cold
+// inputs. With block scales, where each product has four multiply-adds behind it and no tile is
+// larger than 256 x 128, 4096^3 takes 74 to 78 against 51 to 53. For float32 outputs of
+// 8-bit inputs both operands are widened at every use: 4096 x 4096 x 8192 307 to 318 with row
+// scales, 339 to 353 with block scales. At the tiles of 128 x 128, by what a compute unit
+// takes into LDS (32 KB a stage at some 75 KB/us).
 #pragma once
 
 #include "lds_load.hpp"

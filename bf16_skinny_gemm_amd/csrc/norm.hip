@@ -152,7 +152,7 @@ __device__ __forceinline__ void store8(uint8_t *p, const u32x2 &v, int left)
 // WPR waves per row, P pieces of 8 columns per lane: covers D <= WPR * 64 * 8 * P. Piece p
 // of a lane is p * WPR * 64 + lane, so a wave reads 1 KiB at a time and 16 neighbouring
 // lanes hold 128 consecutive columns: a scale group is a 16-lane row. 1 x 4096 with residual
-// takes 1.9 us (a launch alone 1.6), 8192 x 4096 with residual to e4m3 38.9 us: 6.0 TB/s.
+// takes 2.0 us, 8192 x 4096 with residual to e4m3 39.2 us: 6.0 TB/s.
 template <int WPR, int P, bool RES, int OUT, bool NT>
 __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArgs a)
 {
