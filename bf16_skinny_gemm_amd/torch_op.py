@@ -333,9 +333,10 @@ class _RoutedProduct(TorchFunctionMode):
         self.weight, self.fallback = weight, fallback
 
     def __torch_function__(self, func, types, args=(), kwargs=None):
-        if func is torch.nn.functional.linear and len(args) == 3 and args[1] is self.weight:
-            return skinny_linear(*args, fallback=self.fallback)
-        return func(*args, **(kwargs or {}))
+        kwargs = kwargs or {}
+        if func is torch.nn.functional.linear and len(args) >= 2 and args[1] is self.weight:
+            return skinny_linear(*args, **kwargs, fallback=self.fallback)
+        return func(*args, **kwargs)
 
 
 def _linear_forward(self, inp, fallback):
@@ -347,7 +348,7 @@ def _linear_forward(self, inp, fallback):
 
 def _own_linear_forward(self, *args, _skinny_fallback, **kwargs):
     """The forward of a class derived from nn.Linear, with its weight's product routed."""
-    with _RoutedProduct(self.weight, _skinny_fallback):
+    with _RoutedProduct(getattr(self, "weight", None), _skinny_fallback):
         return type(self).forward(self, *args, **kwargs)
 
 

@@ -242,3 +242,38 @@ def test_fused_leaves_odd_widths_to_the_standard_path(op):
         assert torch.equal(layer(x), want)
         y = layer(torch.randn(4, 1008, device="cuda").to(torch.bfloat16)[:, :1001])
         assert y.shape == (4, 64)
+
+
+class Packed(torch.nn.Linear):
+    """Its weight in another form, as quantised layers keep it."""
+
+    def __init__(self, *args, **kwargs):
+        super().__init__(*args, **kwargs)
+        self.packed = torch.nn.Parameter(self.weight.detach() * 3)
+        del self.weight
+
+    def forward(self, x):
+        return torch.nn.functional.linear(x, self.packed / 3, self.bias)
+
+
+def test_a_linear_class_without_a_weight(op):
+    torch.manual_seed(0)
+    layer, x = Packed(8, 4), torch.randn(2, 8)
+    want = layer(x)
+    op.install(torch.nn.Sequential(layer))
+    assert torch.equal(layer(x), want)
+
+
+@pytest.mark.parametrize("call", [lambda f, x, s: f(x, s.weight) + s.bias, lambda f, x, s: f(x, s.weight, bias=s.bias),
+                                  lambda f, x, s: f(x, s.weight, None) + s.bias])
+def test_every_form_of_the_product_is_routed(op, monkeypatch, call):
+    class Own(torch.nn.Linear):
+        def forward(self, x):
+            return call(torch.nn.functional.linear, x, self)
+
+    torch.manual_seed(0)
+    layer, x = Own(8, 4), torch.randn(2, 8)
+    want, seen, plain = layer(x), [], op.skinny_linear
+    op.install(torch.nn.Sequential(layer))
+    monkeypatch.setattr(op, "skinny_linear", lambda *a, **k: (seen.append(a), plain(*a, **k))[1])
+    assert torch.equal(layer(x), want) and len(seen) == 1
