@@ -18,11 +18,13 @@ Python ints; a non-zero status raises :class:`SkinnyError`):
     skinny_gemm_bf16_split_k_noalloc, skinny_gemm_split_k_num_variants,
     skinny_gemm_split_k_get_variant, skinny_gemm_split_k_default_plan,
     skinny_rms_norm_bf16, skinny_rms_norm_fp8, skinny_linear_bf16, skinny_linear_fp8,
-    skinny_linear_default_plan
+    skinny_linear_default_plan, skinny_rms_norm_int8, skinny_quantize_int8, skinny_linear_int8,
+    skinny_linear_int8_default_plan
 
 Tensor helpers: :func:`gemm`, :func:`gemm_pair`, :func:`gemm_pair_strided`,
 :func:`split_k_workspace`, :func:`gemm_split_k` and :func:`gemm_split_k_noalloc`;
-:func:`rms_norm` and :func:`linear` (any number of rows, ``include/skinny_ops.h``).
+:func:`rms_norm`, :func:`quantize_int8` and :func:`linear` (any number of rows,
+``include/skinny_ops.h``).
 """
 from __future__ import annotations
 
@@ -176,12 +178,14 @@ def lib() -> ctypes.CDLL:
         L.skinny_gemm_split_k_get_variant.argtypes = [i, pp]
         L.skinny_gemm_split_k_default_plan.argtypes = [i, i, i, pp]
         for name, args in (("skinny_rms_norm_bf16", NormArgs), ("skinny_rms_norm_fp8", NormArgs),
-                           ("skinny_linear_bf16", LinearArgs), ("skinny_linear_fp8", LinearArgs)):
+                           ("skinny_rms_norm_int8", NormArgs), ("skinny_quantize_int8", NormArgs),
+                           ("skinny_linear_bf16", LinearArgs), ("skinny_linear_fp8", LinearArgs),
+                           ("skinny_linear_int8", LinearArgs)):
             getattr(L, name).argtypes = [ctypes.POINTER(args), vp]
             getattr(L, name).restype = ctypes.c_int
-        L.skinny_linear_default_plan.argtypes = [ctypes.POINTER(LinearArgs), ctypes.c_int32,
-                                                 ctypes.POINTER(LinearPlan)]
-        L.skinny_linear_default_plan.restype = ctypes.c_int
+        for name in ("skinny_linear_default_plan", "skinny_linear_int8_default_plan"):
+            getattr(L, name).argtypes = [ctypes.POINTER(LinearArgs), ctypes.c_int32, ctypes.POINTER(LinearPlan)]
+            getattr(L, name).restype = ctypes.c_int
         for name in ("skinny_gemm_init", "skinny_gemm_bf16", "skinny_gemm_bf16_pair",
                      "skinny_gemm_bf16_ex", "skinny_gemm_bf16_pair_ex", "skinny_gemm_bf16_f32out",
                      "skinny_gemm_bf16_f32out_ex", "skinny_gemm_bf16_pair_strided",
@@ -339,6 +343,14 @@ def skinny_rms_norm_fp8(args: NormArgs, stream: int = 0) -> None:
     _check(lib().skinny_rms_norm_fp8(ctypes.byref(args), stream), "skinny_rms_norm_fp8")
 
 
+def skinny_rms_norm_int8(args: NormArgs, stream: int = 0) -> None:
+    _check(lib().skinny_rms_norm_int8(ctypes.byref(args), stream), "skinny_rms_norm_int8")
+
+
+def skinny_quantize_int8(args: NormArgs, stream: int = 0) -> None:
+    _check(lib().skinny_quantize_int8(ctypes.byref(args), stream), "skinny_quantize_int8")
+
+
 def skinny_linear_bf16(args: LinearArgs, stream: int = 0) -> None:
     _check(lib().skinny_linear_bf16(ctypes.byref(args), stream), "skinny_linear_bf16")
 
@@ -347,10 +359,21 @@ def skinny_linear_fp8(args: LinearArgs, stream: int = 0) -> None:
     _check(lib().skinny_linear_fp8(ctypes.byref(args), stream), "skinny_linear_fp8")
 
 
+def skinny_linear_int8(args: LinearArgs, stream: int = 0) -> None:
+    _check(lib().skinny_linear_int8(ctypes.byref(args), stream), "skinny_linear_int8")
+
+
 def skinny_linear_default_plan(args: LinearArgs, compute_units: int = 256) -> LinearPlan:
     p = LinearPlan()
     _check(lib().skinny_linear_default_plan(ctypes.byref(args), compute_units, ctypes.byref(p)),
            "skinny_linear_default_plan")
+    return p
+
+
+def skinny_linear_int8_default_plan(args: LinearArgs, compute_units: int = 256) -> LinearPlan:
+    p = LinearPlan()
+    _check(lib().skinny_linear_int8_default_plan(ctypes.byref(args), compute_units, ctypes.byref(p)),
+           "skinny_linear_int8_default_plan")
     return p
 
 
@@ -620,15 +643,15 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     y = h * weight / sqrt(mean(h^2) + eps), one kernel launch on the current stream.
 
     quant None: y is bfloat16. quant "row" or "group": y is float8_e4m3fn with float32
-    scales per row ([M]) or per 128 columns ([M, ceil(D / 128)]). Returns y, or (y, scale)
-    with quant; with a residual the new residual h (bfloat16) is returned last. out, scale
+    scales per row ([M]) or per 128 columns ([M, ceil(D / 128)]). quant "int8": y is int8 with
+    float32 scales per row. Returns y, or (y, scale) with quant; with a residual the new residual h (bfloat16) is returned last. out, scale
     and residual_out may be given; residual_out may be residual or x, and out may be x."""
     ldx = _matrix(x, "x", torch.bfloat16, None)
     M, D = x.shape
     if D == 0:
         raise ValueError("the width must be above 0")
-    if quant not in (None, "row", "group"):
-        raise ValueError(f"quant must be None, 'row' or 'group', got {quant!r}")
+    if quant not in (None, "row", "group", "int8"):
+        raise ValueError(f"quant must be None, 'row', 'group' or 'int8', got {quant!r}")
     if residual is None and residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if quant is None and scale is not None:
@@ -637,7 +660,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     a.weight = _vector(weight, "weight", torch.bfloat16, x.device, (D,))
     if weight is None:
         raise TypeError("weight must be a torch.Tensor")
-    dtype = torch.bfloat16 if quant is None else torch.float8_e4m3fn
+    dtype = torch.bfloat16 if quant is None else torch.int8 if quant == "int8" else torch.float8_e4m3fn
     if out is None:
         out = torch.empty((M, D), dtype=dtype, device=x.device)
     a.ldy = _matrix(out, "out", dtype, x.device, (M, D))
@@ -651,7 +674,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         a.residual_out = residual_out.data_ptr()
     got = [out]
     if quant is not None:
-        shape = (M,) if quant == "row" else (M, -(-D // 128))
+        shape = (M, -(-D // 128)) if quant == "group" else (M,)
         if scale is None:
             scale = torch.empty(shape, dtype=torch.float32, device=x.device)
         a.scale = _vector(scale, "scale", torch.float32, x.device, shape)
@@ -660,8 +683,31 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         got.append(residual_out)
     s = _stream_handle(x.device)
     with _on_device(x.device):
-        (skinny_rms_norm_bf16 if quant is None else skinny_rms_norm_fp8)(a, s)
+        (skinny_rms_norm_bf16 if quant is None else
+         skinny_rms_norm_int8 if quant == "int8" else skinny_rms_norm_fp8)(a, s)
     return got[0] if len(got) == 1 else tuple(got)
+
+
+def quantize_int8(x: torch.Tensor, out: torch.Tensor | None = None,
+                  scale: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(q, scale): the rows of bfloat16 x [M, D] (rows may be strided) as int8 [M, D] with one
+    float32 scale each [M], the row's largest magnitude / 127; one kernel launch on the
+    current stream. out and scale may be given."""
+    ldx = _matrix(x, "x", torch.bfloat16, None)
+    M, D = x.shape
+    if D == 0:
+        raise ValueError("the width must be above 0")
+    if out is None:
+        out = torch.empty((M, D), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty((M,), dtype=torch.float32, device=x.device)
+    a = NormArgs(x=x.data_ptr(), ldx=ldx, M=M, D=D, y=out.data_ptr(),
+                 ldy=_matrix(out, "out", torch.int8, x.device, (M, D)),
+                 scale=_vector(scale, "scale", torch.float32, x.device, (M,)))
+    s = _stream_handle(x.device)
+    with _on_device(x.device):
+        skinny_quantize_int8(a, s)
+    return out, scale
 
 
 def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None,
@@ -674,12 +720,14 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None,
     strided), or the gated form act(x @ W.T + bias) * (x @ W_up.T + bias_up); one kernel
     launch on the current stream.
 
-    x and W are bfloat16, or float8_e4m3fn with float32 scales: per row (x_scale [M],
+    x and W are bfloat16, or int8 with float32 scales per row (x_scale [M], w_scale [N]; K at
+    most 131071), or float8_e4m3fn with float32 scales: per row (x_scale [M],
     w_scale [N]) or per 128 columns of x and 128 x 128 block of W (x_scale
     [M, ceil(K/128)], w_scale [ceil(N/128), ceil(K/128)]). act: none, relu, gelu,
     gelu_tanh or silu. out may be given; a bfloat16 out may be the residual itself."""
+    int8 = isinstance(x, torch.Tensor) and x.dtype == torch.int8
     fp8 = isinstance(x, torch.Tensor) and x.dtype == torch.float8_e4m3fn
-    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    dtype = x.dtype if int8 or fp8 else torch.bfloat16
     ldx = _matrix(x, "x", dtype, None)
     M, K = x.shape
     if act not in ACTS:
@@ -696,18 +744,20 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None,
         raise ValueError("the gated form takes no residual")
     if W_up is not None and N * K == 0 and M > 0:
         raise ValueError("the gated form needs N and K above 0")
-    if not fp8 and not (x_scale is None and w_scale is None and w_up_scale is None):
-        raise ValueError("scales belong to float8_e4m3fn inputs")
+    if int8 and K > 131071:
+        raise ValueError(f"int8 sums hold at most 131071 products, got {K}")
+    if not (int8 or fp8) and not (x_scale is None and w_scale is None and w_up_scale is None):
+        raise ValueError("scales belong to float8_e4m3fn and int8 inputs")
     a = LinearArgs(x=x.data_ptr(), ldx=ldx, M=M, N=N, K=K, act=ACTS[act],
                    out_f32=out_dtype == torch.float32)
     a.W0 = _vector(W, "W", dtype, x.device, (N, K))
     a.W1 = _vector(W_up, "W_up", dtype, x.device, (N, K))
     a.bias0 = _vector(bias, "bias", torch.bfloat16, x.device, (N,))
     a.bias1 = _vector(bias_up, "bias_up", torch.bfloat16, x.device, (N,))
-    if fp8:
+    if int8 or fp8:
         if x_scale is None or w_scale is None or (W_up is not None) != (w_up_scale is not None):
-            raise ValueError("float8_e4m3fn inputs need x_scale and a scale for each weight")
-        blocks = w_scale.dim() == 2
+            raise ValueError(f"{dtype} inputs need x_scale and a scale for each weight")
+        blocks = fp8 and w_scale.dim() == 2
         kb, nb = -(-K // 128), -(-N // 128)
         a.scales = SKINNY_SCALES_BLOCK if blocks else SKINNY_SCALES_ROW
         ws = (nb, kb) if blocks else (N,)
@@ -723,7 +773,7 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None,
     a.y = out.data_ptr()
     s = _stream_handle(x.device)
     with _on_device(x.device):
-        (skinny_linear_fp8 if fp8 else skinny_linear_bf16)(a, s)
+        (skinny_linear_fp8 if fp8 else skinny_linear_int8 if int8 else skinny_linear_bf16)(a, s)
     return out
 
 
@@ -742,7 +792,8 @@ __all__ = [
     "SKINNY_ERR_LAUNCH", "SKINNY_KIND_FIXED_K", "SKINNY_KIND_LOOP_K", "SKINNY_KIND_SCALAR",
     "SKINNY_KIND_MFMA", "NormArgs", "LinearArgs", "LinearPlan", "ACTS", "rms_norm", "linear",
     "skinny_rms_norm_bf16", "skinny_rms_norm_fp8", "skinny_linear_bf16", "skinny_linear_fp8",
-    "skinny_linear_default_plan", "SKINNY_LINEAR_ELEMENTS", "SKINNY_LINEAR_STREAM", "SKINNY_LINEAR_TILE",
+    "skinny_linear_default_plan", "quantize_int8", "skinny_rms_norm_int8", "skinny_quantize_int8",
+    "skinny_linear_int8", "skinny_linear_int8_default_plan", "SKINNY_LINEAR_ELEMENTS", "SKINNY_LINEAR_STREAM", "SKINNY_LINEAR_TILE",
     "SKINNY_ACT_NONE", "SKINNY_ACT_RELU", "SKINNY_ACT_GELU", "SKINNY_ACT_GELU_TANH",
     "SKINNY_ACT_SILU", "SKINNY_SCALES_ROW", "SKINNY_SCALES_BLOCK",
 ]

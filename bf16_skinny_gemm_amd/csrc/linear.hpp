@@ -1,4 +1,4 @@
-// Device code shared by the kernels of skinny_linear_bf16 / _fp8 (include/skinny_ops.h):
+// Device code shared by the kernels of skinny_linear_bf16 / _fp8 / _int8 (include/skinny_ops.h):
 // arguments, the epilogue, and the matrix instructions on bytes.
 #pragma once
 
@@ -15,7 +15,19 @@ namespace skg {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// The kernels' MODE: the type of x and W, and their scales.
+enum { kBf16 = 0, kE4m3Row = 1, kE4m3Block = 2, kInt8Row = 3 };
+constexpr bool row_scaled(int mode) { return mode == kE4m3Row || mode == kInt8Row; }
+
+// The running sums of four outputs: 32-bit integers for 8-bit integer products, exact for
+// any K of the entry point (at most 131071 products of at most 2^14).
+template <int MODE>
+using sums_t = std::conditional_t<MODE == kInt8Row, i32x4, f32x4>;
+__device__ __forceinline__ f32x4 to_f32(const f32x4 &v) { return v; }
+__device__ __forceinline__ f32x4 to_f32(const i32x4 &v) { return __builtin_convertvector(v, f32x4); }
 
 struct LinArgs {
     const uint8_t *x, *w[2];
@@ -134,7 +146,7 @@ __device__ __forceinline__ u32x2 residual4(const LinArgs &a, int m, int n)
 }
 
 // Four consecutive outputs n .. n + 3 of row m, of which any may lie beyond N. The sums have
-// yet to be multiplied by their scales (MODE 1), xs that of the row.
+// yet to be multiplied by their scales (row_scaled), xs that of the row.
 template <int MODE, bool GATED>
 __device__ __forceinline__ void finish4(const LinArgs &a, f32x4 z, f32x4 u, u32x2 r, float xs, int m, int n)
 {
@@ -144,7 +156,7 @@ __device__ __forceinline__ void finish4(const LinArgs &a, f32x4 z, f32x4 u, u32x
             if (n + e >= a.N)
                 continue;
             float z1 = z[e], u1 = u[e];
-            if constexpr (MODE == 1) {
+            if constexpr (row_scaled(MODE)) {
                 z1 *= xs * a.ws[0][n + e];
                 if constexpr (GATED)
                     u1 *= xs * a.ws[1][n + e];
@@ -153,7 +165,7 @@ __device__ __forceinline__ void finish4(const LinArgs &a, f32x4 z, f32x4 u, u32x
         }
         return;
     }
-    if constexpr (MODE == 1) {
+    if constexpr (row_scaled(MODE)) {
         const f32x4 s0 = *reinterpret_cast<const f32x4_any *>(a.ws[0] + n);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -198,7 +210,7 @@ struct Columns8 {
         for (int q = 0; q < 1 + GATED; ++q)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if constexpr (MODE == 1)
+                if constexpr (row_scaled(MODE))
                     s[q][h] = wide ? *reinterpret_cast<const f32x4_any *>(a.ws[q] + n + 4 * h) : f32x4{0, 0, 0, 0};
                 b[q][h] = wide && a.bias[q] ? *reinterpret_cast<const u32x2_any *>(a.bias[q] + n + 4 * h) : u32x2{0, 0};
             }
@@ -210,7 +222,7 @@ struct Columns8 {
         for (int q = 0; q < 1 + GATED; ++q)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if constexpr (MODE == 1)
+                if constexpr (row_scaled(MODE))
                     asm volatile("" : "+v"(s[q][h]));
                 asm volatile("" : "+v"(b[q][h]));
             }
@@ -220,7 +232,7 @@ struct Columns8 {
         float v[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if constexpr (MODE == 1)
+            if constexpr (row_scaled(MODE))
                 z[h] *= s[0][h];
             z[h] += widen4(b[0][h]);
 #pragma unroll
@@ -232,7 +244,7 @@ struct Columns8 {
         for (int h = 0; h < 2; ++h) {
             z[h] = f32x4{v[h * 4], v[h * 4 + 1], v[h * 4 + 2], v[h * 4 + 3]};
             if constexpr (GATED) {
-                if constexpr (MODE == 1)
+                if constexpr (row_scaled(MODE))
                     u[h] *= s[GATED][h];
                 z[h] *= u[h] + widen4(b[GATED][h]);
             } else {
@@ -270,6 +282,15 @@ __device__ __forceinline__ f32x4 mfma_fp8(const u32x4 &a0, const u32x4 &a1, cons
     // formats 0 = e4m3 for both; scale operands 0 select the form without scales
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
+
+__device__ __forceinline__ i32x4 mfma_int8(const u32x4 &a, const u32x4 &b, const i32x4 &c)
+{
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+// One of the two products of a lane's 32 bytes, where each takes 16 of them.
+__device__ __forceinline__ f32x4 mfma_half(const u32x4 &a, const u32x4 &b, const f32x4 &c) { return mfma_bf16(a, b, c); }
+__device__ __forceinline__ i32x4 mfma_half(const u32x4 &a, const u32x4 &b, const i32x4 &c) { return mfma_int8(a, b, c); }
 
 // Sixteen e4m3 values as bfloat16, which holds each of them (v_cvt_scalef32_pk_bf16_fp8).
 __device__ __forceinline__ void widen(const u32x4 &v, u32x4 &lo, u32x4 &hi)
@@ -334,8 +355,10 @@ constexpr int kTileMost = 4;
 int stream_kernels_bf16(int M, bool gated, bool exact, StreamKernel *out);
 int stream_kernels_row(int M, bool gated, bool exact, StreamKernel *out);
 int stream_kernels_block(int M, bool gated, bool exact, StreamKernel *out);
+int stream_kernels_int8(int M, bool gated, StreamKernel *out);
 int tile_kernels_bf16(bool gated, bool exact, TileKernel *out);
 int tile_kernels_row(bool gated, bool exact, TileKernel *out);
 int tile_kernels_block(bool gated, bool exact, TileKernel *out);
+int tile_kernels_int8(bool gated, TileKernel *out);
 
 }  // namespace skg_host

@@ -19,7 +19,7 @@
 
 namespace skg {
 
-// MODE: 0 bfloat16, 1 e4m3 with row scales, 2 e4m3 with block scales; EXACT: see
+// MODE: see linear.hpp; EXACT: see
 // mfma_bytes. A block computes NB output features (of each
 // weight, GATED) of TM * 16 rows with WAVES waves. NB = 8 fills half of an instruction's
 // rows, or one half with each weight; NB = 4 (GATED) both weights' rows in one half, for
@@ -29,7 +29,7 @@ namespace skg {
 template <int MODE, bool EXACT, bool GATED, int NB, int TM, int XR, int RING, int WAVES, bool NT>
 __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, int nt, int mt)
 {
-    constexpr bool FP8 = MODE != 0, BLOCK = MODE == 2;
+    constexpr bool BLOCK = MODE == kE4m3Block, HALVES = MODE == kBf16 || MODE == kInt8Row;
     constexpr int MATS = GATED ? 2 : 1;
     constexpr bool HALF = NB == 8, QUARTER = NB == 4;
     static_assert(!QUARTER || GATED, "a load takes 8 rows");
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
     const int t = xcd * q8 + (xcd < r8 ? xcd : r8) + (int)(blockIdx.x / 8);
     const int n0 = t / mt * NB, m0 = t % mt * BM;
 
-    const int KB = FP8 ? a.K : a.K * 2;
+    const int KB = MODE == kBf16 ? a.K * 2 : a.K;
     const int stages = (KB + 127) / 128;
     const int vn = a.N - n0 < NB ? a.N - n0 : NB;
     const int vm = a.M - m0 < BM ? a.M - m0 : BM;
@@ -112,12 +112,13 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
         }
     };
 
-    f32x4 acc[TN][TM];
+    using sums = sums_t<MODE>;
+    sums acc[TN][TM];
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j)
-            acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            acc[i][j] = sums{0, 0, 0, 0};
     const int p0 = (g ^ (i16 & 7)) * 16, p1 = ((g + 4) ^ (i16 & 7)) * 16;
 
 #pragma unroll
@@ -161,10 +162,10 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
         for (int i = 0; i < TN; ++i)
 #pragma unroll
             for (int j = 0; j < TM; ++j) {
-                f32x4 &c = acc[i][j];
-                if constexpr (!FP8) {
-                    c = mfma_bf16(af[i][0], bf[j][0], c);
-                    c = mfma_bf16(af[i][1], bf[j][1], c);
+                sums &c = acc[i][j];
+                if constexpr (HALVES) {
+                    c = mfma_half(af[i][0], bf[j][0], c);
+                    c = mfma_half(af[i][1], bf[j][1], c);
                 } else if constexpr (!BLOCK) {
                     c = mfma_bytes<EXACT>(af[i], bf[j], c);
                 } else {
@@ -178,7 +179,7 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
 
     // the waves' sums meet in LDS, added in the order of the waves
     __syncthreads();
-    f32x4 *part = reinterpret_cast<f32x4 *>(smem);
+    sums *part = reinterpret_cast<sums *>(smem);
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -192,14 +193,14 @@ __global__ __launch_bounds__(WAVES * 64) void linear_stream_kernel(LinArgs a, in
         if (m >= a.M || n >= a.N)
             continue;
         const u32x2 r = residual4(a, m, n);
-        f32x4 z = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, u = z;
+        sums z = sums{0, 0, 0, 0}, u = z;
 #pragma unroll
         for (int k = 0; k < WAVES; ++k) {
             z += part[((k * TN + i) * TM + j) * 64 + l];
             if constexpr (GATED)
                 u += HALF || QUARTER ? part[(k * TM + j) * 64 + SLOTS + l] : part[((k * TN + TF + i) * TM + j) * 64 + l];
         }
-        finish4<MODE, GATED>(a, z, u, r, MODE == 1 ? a.xs[m] : 1.0f, m, n);
+        finish4<MODE, GATED>(a, to_f32(z), to_f32(u), r, row_scaled(MODE) ? a.xs[m] : 1.0f, m, n);
     }
 }
 
@@ -211,7 +212,7 @@ template <int MODE, bool EXACT, bool GATED, int NB, int TM, int XR, int RING, in
 StreamKernel stream_of()
 {
     constexpr int MATS = GATED ? 2 : 1, BN = NB * MATS, TN = (BN + 15) / 16;
-    constexpr int STAGE = (BN + XR) * 128 + (MODE == 2 ? ((TM + 3) / 4 + MATS) * 256 : 0);
+    constexpr int STAGE = (BN + XR) * 128 + (MODE == skg::kE4m3Block ? ((TM + 3) / 4 + MATS) * 256 : 0);
     constexpr int RINGS = WAVES * RING * STAGE, PART = WAVES * TN * TM * 1024;
     return StreamKernel{
         reinterpret_cast<const void *>(&skg::linear_stream_kernel<MODE, EXACT, GATED, NB, TM, XR, RING, WAVES, NT>),
@@ -223,7 +224,7 @@ StreamKernel stream_of()
 template <int MODE, bool EXACT, bool GATED>
 int stream_set(int M, StreamKernel *out)
 {
-    constexpr bool E = MODE != 0;
+    constexpr bool E = MODE == skg::kE4m3Row || MODE == skg::kE4m3Block;
     int n = 0;
     if (M <= 8) {
         out[n++] = stream_of<MODE, E, GATED, 8, 1, 8, 2, 8, true>();
@@ -246,7 +247,7 @@ int stream_set(int M, StreamKernel *out)
         out[n++] = stream_of<MODE, EXACT, GATED, 32, 2, 32, 2, 4, false>();
         out[n++] = stream_of<MODE, EXACT, GATED, 32, 4, 64, 1, 4, false>();
         out[n++] = stream_of<MODE, EXACT, GATED, 32, 4, 64, 1, 8, false>();
-        if constexpr (!(EXACT && MODE == 2))  // where the registers hold it
+        if constexpr (!(EXACT && MODE == skg::kE4m3Block))  // where the registers hold it
             out[n++] = stream_of<MODE, EXACT, GATED, GATED ? 32 : 64, 6, 96, 1, 6, false>();
         if constexpr (!GATED) {
             out[n++] = stream_of<MODE, EXACT, GATED, 64, 3, 48, 1, 4, false>();
@@ -261,7 +262,7 @@ int stream_set(int M, StreamKernel *out)
 template <int MODE>
 int stream_pick(int M, bool gated, bool exact, StreamKernel *out)
 {
-    if constexpr (MODE != 0)
+    if constexpr (MODE == skg::kE4m3Row || MODE == skg::kE4m3Block)
         if (exact)
             return gated ? stream_set<MODE, true, true>(M, out) : stream_set<MODE, true, false>(M, out);
     return gated ? stream_set<MODE, false, true>(M, out) : stream_set<MODE, false, false>(M, out);

@@ -47,7 +47,7 @@ namespace skg {
 template <int MODE, bool EXACT, bool GATED, int WN, int WM, int TN, int TM>
 __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int nt, int mt)
 {
-    constexpr bool FP8 = MODE != 0, BLOCK = MODE == 2;
+    constexpr bool BLOCK = MODE == kE4m3Block, HALVES = MODE == kBf16 || MODE == kInt8Row;
     constexpr bool PINNED = !BLOCK;  // products and reads of a stage stay in source order
     constexpr int WAVES = WN * WM;
     constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
     const int rows = mt - first < GROUP ? mt - first : GROUP;
     const int n0 = (t % per) / rows * NB, m0 = (first + (t % per) % rows) * BM;
 
-    const int KB = FP8 ? a.K : a.K * 2;
+    const int KB = MODE == kBf16 ? a.K * 2 : a.K;
     const int stages = (KB + 127) / 128;
     const int vn = a.N - n0 < NB ? a.N - n0 : NB;
     const int vm = a.M - m0 < BM ? a.M - m0 : BM;
@@ -149,12 +149,13 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
         }
     };
 
-    f32x4 acc[TN][TM];
+    using sums = sums_t<MODE>;
+    sums acc[TN][TM];
 #pragma unroll
     for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j)
-            acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            acc[i][j] = sums{0, 0, 0, 0};
 
     // this lane's pieces of a fragment's row; piece p of row r is at p ^ (r % 8)
     const int p0 = (g ^ (i16 & 7)) * 16, p1 = ((g + 4) ^ (i16 & 7)) * 16;
@@ -180,16 +181,16 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
             if constexpr (i + 1 < TN)
                 read_a(st, i + 1, af[(i + 1) & 1]);
             // the two products of a sum stay TM apart: back to back, the second would wait
-            if constexpr (!FP8)
+            if constexpr (HALVES)
                 static_for<0, TM>([&](auto jc) {
                     constexpr int j = decltype(jc)::value;
-                    acc[i][j] = mfma_bf16(af[i & 1][0], bf[P][j][0], acc[i][j]);
+                    acc[i][j] = mfma_half(af[i & 1][0], bf[P][j][0], acc[i][j]);
                 });
             static_for<0, TM>([&](auto jc) {
                 constexpr int j = decltype(jc)::value;
-                f32x4 &c = acc[i][j];
-                if constexpr (!FP8) {
-                    c = mfma_bf16(af[i & 1][1], bf[P][j][1], c);
+                sums &c = acc[i][j];
+                if constexpr (HALVES) {
+                    c = mfma_half(af[i & 1][1], bf[P][j][1], c);
                 } else if constexpr (!BLOCK) {
                     c = mfma_bytes<EXACT>(af[i & 1], bf[P][j], c);
                 } else {
@@ -291,14 +292,12 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
                                          : u32x4{0, 0, 0, 0};
             }
         }
-    if constexpr (MODE == 1) {
+    float xsv[TM];
+    if constexpr (row_scaled(MODE)) {
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
             const int m = m0 + (wm * TM + j) * 16 + i16;
-            const float xs = m < a.M ? a.xs[m] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < TN; ++i)
-                acc[i][j] *= xs;
+            xsv[j] = m < a.M ? a.xs[m] : 0.0f;
         }
     }
     cols.settle();
@@ -312,11 +311,12 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
             static_for<0, TN>([&](auto ic) {
                 constexpr int i = decltype(ic)::value;
                 const int p = ((i / TF) * NB + (wn * TF + i % TF) * 16) / 4 + g;
-                *reinterpret_cast<f32x4 *>(smem + row * (BN * 4) + (p ^ i16) * 16) = acc[i][q * JP + j];
+                *reinterpret_cast<f32x4 *>(smem + row * (BN * 4) + (p ^ i16) * 16) =
+                    row_scaled(MODE) ? to_f32(acc[i][q * JP + j]) * xsv[q * JP + j] : to_f32(acc[i][q * JP + j]);
             });
         });
         __syncthreads();
-        auto sums = [&](int row, f32x4 (&z)[2], f32x4 (&u)[2]) {
+        auto sums_of = [&](int row, f32x4 (&z)[2], f32x4 (&u)[2]) {
             const uint8_t *at_row = smem + row * (BN * 4);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -329,7 +329,7 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
             for (int k = 0; k < ITERS; ++k) {
                 const int row = row_of(k), m = m_of(q, row);
                 f32x4 z[2], u[2];
-                sums(row, z, u);
+                sums_of(row, z, u);
                 if (m < a.M && wide)
                     cols.finish(a, z, u, u32x4{0, 0, 0, 0}, m, n);
             }
@@ -342,7 +342,7 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
             for (int k = 0; k < ITERS; ++k) {
                 const int row = row_of(k), m = m_of(q, row);
                 f32x4 z[2], u[2];
-                sums(row, z, u);
+                sums_of(row, z, u);
                 if (m < a.M && wide)
                     cols.finish(a, z, u, res[q * ITERS + k], m, n);
             }
@@ -354,7 +354,7 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
                 const float *at = reinterpret_cast<const float *>(smem + row * (BN * 4) + c % 4 * 4);
                 if (c < vn && m < a.M) {
                     float z = at[(c / 4 ^ (row & 15)) * 4], u = at[((NB * GATED + c) / 4 ^ (row & 15)) * 4];
-                    if constexpr (MODE == 1) {
+                    if constexpr (row_scaled(MODE)) {
                         z *= a.ws[0][n0 + c];
                         u *= a.ws[GATED][n0 + c];
                     }
@@ -387,11 +387,11 @@ int tile_set(TileKernel *out)
     int n = 0;
     if constexpr (EXACT) {  // for float32 outputs only: one tile serves them
         out[n++] = tile_of<MODE, EXACT, GATED, 2, 2, 4, 4>(1.2f);
-    } else if constexpr (MODE == 2) {
+    } else if constexpr (MODE == skg::kE4m3Block) {
         out[n++] = tile_of<MODE, EXACT, GATED, 2, 2, 4, 2>(0.47f);
         out[n++] = tile_of<MODE, EXACT, GATED, 2, 4, 4, 2>(0.65f);
         out[n++] = tile_of<MODE, EXACT, GATED, 4, 2, 4, 4>(0.87f);
-    } else if constexpr (MODE == 1) {
+    } else if constexpr (skg::row_scaled(MODE)) {
         out[n++] = tile_of<MODE, EXACT, GATED, 2, 2, 4, 2>(0.4f);
         out[n++] = tile_of<MODE, EXACT, GATED, 2, 4, 4, 2>(0.42f);
         out[n++] = tile_of<MODE, EXACT, GATED, 4, 2, 4, 4>(0.72f);
@@ -409,7 +409,7 @@ int tile_set(TileKernel *out)
 template <int MODE>
 int tile_pick(bool gated, bool exact, TileKernel *out)
 {
-    if constexpr (MODE != 0)
+    if constexpr (MODE == skg::kE4m3Row || MODE == skg::kE4m3Block)
         if (exact)
             return gated ? tile_set<MODE, true, true>(out) : tile_set<MODE, true, false>(out);
     return gated ? tile_set<MODE, false, true>(out) : tile_set<MODE, false, false>(out);

@@ -1,5 +1,5 @@
-// Root-mean-square norm with the residual's addition, to bfloat16 or to e4m3 with
-// float32 scales (include/skinny_ops.h).
+// Root-mean-square norm with the residual's addition, to bfloat16, or to e4m3 or 8-bit
+// integers with float32 scales; and rows as they are to 8-bit integers (include/skinny_ops.h).
 //
 //   h = x + residual,   y = h * w / sqrt(mean(h^2) + eps)
 //
@@ -22,7 +22,7 @@
 
 namespace skg {
 
-constexpr float kE4m3Max = 448.0f;
+constexpr float kE4m3Max = 448.0f, kInt8Max = 127.0f;
 constexpr float kLeastAmax = 0x1p-100f;  // keeps 1 / scale finite for a row or group of zeros
 
 struct NormArgs {
@@ -35,7 +35,10 @@ struct NormArgs {
     float eps;
 };
 
-enum { kOutBf16 = 0, kOutRow = 1, kOutGroup = 2 };
+// e4m3 by rows or groups; 8-bit integers by rows, of the norm or of x itself (no weight, no norm)
+enum { kOutBf16 = 0, kOutRow = 1, kOutGroup = 2, kOutInt8 = 3, kOutPlainInt8 = 4 };
+constexpr bool int8_out(int out) { return out == kOutInt8 || out == kOutPlainInt8; }
+constexpr bool row_out(int out) { return out == kOutRow || int8_out(out); }
 
 template <int CTRL>
 __device__ __forceinline__ unsigned dpp_umax(unsigned v)
@@ -80,10 +83,11 @@ __device__ __forceinline__ unsigned wave_umax(unsigned v)
 __device__ __forceinline__ unsigned abs_bits(float v) { return __builtin_bit_cast(unsigned, v) & 0x7FFFFFFFu; }
 
 // scale of the largest |y| (amax >= 0, or NaN).
+template <int OUT>
 __device__ __forceinline__ float scale_of(float amax)
 {
     const float a = amax < kLeastAmax ? kLeastAmax : amax;  // NaN stays
-    return a / kE4m3Max;
+    return a / (int8_out(OUT) ? kInt8Max : kE4m3Max);
 }
 
 // q = e4m3((hw * f) * (1 / scale)), f = 1 / rms. The factors stay apart: f / scale overflows
@@ -96,6 +100,19 @@ __device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d
     int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
     v = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
     return (unsigned)v;
+}
+
+// The same to 8-bit integers, nearest-even: |y / scale| <= 127 (1 + 2^-22), which rounds to
+// 127. NaN gives 0, beside a scale of NaN.
+__device__ __forceinline__ unsigned to_int8(float v) { return (unsigned)(int)__builtin_rintf(v) & 0xFFu; }
+
+template <int OUT>
+__device__ __forceinline__ unsigned pack_bytes(float a, float b, float c, float d)
+{
+    if constexpr (int8_out(OUT))
+        return to_int8(a) | to_int8(b) << 8 | to_int8(c) << 16 | to_int8(d) << 24;
+    else
+        return pack_e4m3(a, b, c, d);
 }
 
 // Eight bfloat16 values from p, of which `left` (> 0) exist: the others are 0. NT: with
@@ -181,7 +198,8 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const int c = (p * LANES + t) * 8;
-        wv[p] = live && c < a.D ? load8<false>(a.w + c, a.D - c) : u32x4{0, 0, 0, 0};
+        if constexpr (OUT != kOutPlainInt8)
+            wv[p] = live && c < a.D ? load8<false>(a.w + c, a.D - c) : u32x4{0, 0, 0, 0};
     }
 
     float hw[P][8];
@@ -199,10 +217,15 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
                 h1 += hi_f32(rv[p][q]);
                 ho[q] = pack_bf16(h0, h1);
             }
-            sum = __builtin_fmaf(h0, h0, sum);
-            sum = __builtin_fmaf(h1, h1, sum);
-            hw[p][2 * q] = h0 * lo_f32(wv[p][q]);
-            hw[p][2 * q + 1] = h1 * hi_f32(wv[p][q]);
+            if constexpr (OUT == kOutPlainInt8) {
+                hw[p][2 * q] = h0;
+                hw[p][2 * q + 1] = h1;
+            } else {
+                sum = __builtin_fmaf(h0, h0, sum);
+                sum = __builtin_fmaf(h1, h1, sum);
+                hw[p][2 * q] = h0 * lo_f32(wv[p][q]);
+                hw[p][2 * q + 1] = h1 * hi_f32(wv[p][q]);
+            }
             if constexpr (OUT != kOutBf16) {
                 const unsigned b0 = abs_bits(hw[p][2 * q]), b1 = abs_bits(hw[p][2 * q + 1]);
                 top[p] = b0 > top[p] ? b0 : top[p];
@@ -217,9 +240,10 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
                 store8<NT>(a.ro + rr * a.ldro + c, ho, a.D - c);
         }
     }
-    sum = wave_sum(sum);
+    if constexpr (OUT != kOutPlainInt8)
+        sum = wave_sum(sum);
     unsigned most = 0;
-    if constexpr (OUT == kOutRow) {
+    if constexpr (row_out(OUT)) {
 #pragma unroll
         for (int p = 0; p < P; ++p)
             most = top[p] > most ? top[p] : most;
@@ -228,23 +252,23 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
     if constexpr (WPR > 1) {
         if (lane == 0) {
             s_sum[wave] = sum;
-            if constexpr (OUT == kOutRow)
+            if constexpr (row_out(OUT))
                 s_max[wave] = most;
         }
         __syncthreads();
         sum = s_sum[sub * WPR];
-        if constexpr (OUT == kOutRow)
+        if constexpr (row_out(OUT))
             most = s_max[sub * WPR];
 #pragma unroll
         for (int k = 1; k < WPR; ++k) {
             sum += s_sum[sub * WPR + k];
-            if constexpr (OUT == kOutRow)
+            if constexpr (row_out(OUT))
                 most = s_max[sub * WPR + k] > most ? s_max[sub * WPR + k] : most;
         }
     }
     if (!live)
         return;
-    const float f = 1.0f / __builtin_sqrtf(sum / (float)a.D + a.eps);
+    const float f = OUT == kOutPlainInt8 ? 1.0f : 1.0f / __builtin_sqrtf(sum / (float)a.D + a.eps);
     if constexpr (OUT == kOutBf16) {
         uint16_t *y = static_cast<uint16_t *>(a.y) + rr * a.ldy;
 #pragma unroll
@@ -260,8 +284,8 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
     } else {
         uint8_t *y = static_cast<uint8_t *>(a.y) + rr * a.ldy;
         float sc = 0.0f, g = 0.0f;
-        if constexpr (OUT == kOutRow) {
-            sc = scale_of(__builtin_bit_cast(float, most) * f);
+        if constexpr (row_out(OUT)) {
+            sc = scale_of<OUT>(__builtin_bit_cast(float, most) * f);
             g = 1.0f / sc;
             if (t == 0)
                 a.scale[row] = sc;
@@ -270,14 +294,14 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
         for (int p = 0; p < P; ++p) {
             const int c = (p * LANES + t) * 8;
             if constexpr (OUT == kOutGroup) {
-                sc = scale_of(__builtin_bit_cast(float, umax16(top[p])) * f);
+                sc = scale_of<OUT>(__builtin_bit_cast(float, umax16(top[p])) * f);
                 g = 1.0f / sc;
                 if ((lane & 15) == 0 && c < a.D)
                     a.scale[rr * a.groups + (c >> 7)] = sc;
             }
             u32x2 o;
-            o[0] = pack_e4m3(hw[p][0] * f * g, hw[p][1] * f * g, hw[p][2] * f * g, hw[p][3] * f * g);
-            o[1] = pack_e4m3(hw[p][4] * f * g, hw[p][5] * f * g, hw[p][6] * f * g, hw[p][7] * f * g);
+            o[0] = pack_bytes<OUT>(hw[p][0] * f * g, hw[p][1] * f * g, hw[p][2] * f * g, hw[p][3] * f * g);
+            o[1] = pack_bytes<OUT>(hw[p][4] * f * g, hw[p][5] * f * g, hw[p][6] * f * g, hw[p][7] * f * g);
             if (c < a.D)
                 store8<NT>(y + c, o, a.D - c);
         }
@@ -300,12 +324,13 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a)
     __shared__ float s_sum[4];
     __shared__ unsigned s_max[4];
     auto h_at = [&](int i) { return RES ? bf16_to_f32(x[i]) + bf16_to_f32(r[i]) : bf16_to_f32(x[i]); };
+    auto weighted = [&](float h, int i) { return OUT == kOutPlainInt8 ? h : h * bf16_to_f32(a.w[i]); };
     float sum = 0.0f;
     unsigned most = 0;
     for (int64_t i = t; i < a.D; i += 256) {
         const float h = h_at((int)i);
         sum = __builtin_fmaf(h, h, sum);
-        const unsigned b = abs_bits(h * bf16_to_f32(a.w[i]));
+        const unsigned b = abs_bits(weighted(h, (int)i));
         most = b > most ? b : most;
     }
     sum = wave_sum(sum);
@@ -319,7 +344,7 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a)
     most = 0;
     for (int k = 0; k < 4; ++k)
         most = s_max[k] > most ? s_max[k] : most;
-    const float f = 1.0f / __builtin_sqrtf(sum / (float)a.D + a.eps);
+    const float f = OUT == kOutPlainInt8 ? 1.0f : 1.0f / __builtin_sqrtf(sum / (float)a.D + a.eps);
     auto store_h = [&](int i, float h) {
         if constexpr (RES)
             a.ro[row * a.ldro + i] = f32_to_bf16(h);
@@ -333,14 +358,14 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a)
         }
     } else {
         uint8_t *y = static_cast<uint8_t *>(a.y) + row * a.ldy;
-        if constexpr (OUT == kOutRow) {
-            const float sc = scale_of(__builtin_bit_cast(float, most) * f), g = 1.0f / sc;
+        if constexpr (row_out(OUT)) {
+            const float sc = scale_of<OUT>(__builtin_bit_cast(float, most) * f), g = 1.0f / sc;
             if (t == 0)
                 a.scale[row] = sc;
             for (int64_t i = t; i < a.D; i += 256) {
                 const float h = h_at((int)i);
                 store_h((int)i, h);
-                y[i] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(h * bf16_to_f32(a.w[i]) * f * g, 0.0f, 0, false);
+                y[i] = (uint8_t)pack_bytes<OUT>(weighted(h, (int)i) * f * g, 0.0f, 0.0f, 0.0f);
             }
         } else {
             // a wave takes a group of 128 columns, two per lane
@@ -355,7 +380,7 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a)
                     const unsigned b = abs_bits(v[k]);
                     top = b > top ? b : top;
                 }
-                const float sc = scale_of(__builtin_bit_cast(float, wave_umax(top)) * f), g = 1.0f / sc;
+                const float sc = scale_of<OUT>(__builtin_bit_cast(float, wave_umax(top)) * f), g = 1.0f / sc;
                 if (lane == 0)
                     a.scale[row * a.groups + g0] = sc;
 #pragma unroll
@@ -385,12 +410,12 @@ template <int WPR, int P, bool NT>
 const void *norm_fn_of(bool res, int out)
 {
     using namespace skg;
-    static const void *const fn[2][3] = {
+    static const void *const fn[2][4] = {
         {(const void *)&norm_kernel<WPR, P, false, 0, NT>, (const void *)&norm_kernel<WPR, P, false, 1, NT>,
-         (const void *)&norm_kernel<WPR, P, false, 2, NT>},
+         (const void *)&norm_kernel<WPR, P, false, 2, NT>, (const void *)&norm_kernel<WPR, P, false, 3, NT>},
         {(const void *)&norm_kernel<WPR, P, true, 0, NT>, (const void *)&norm_kernel<WPR, P, true, 1, NT>,
-         (const void *)&norm_kernel<WPR, P, true, 2, NT>}};
-    return fn[res][out];
+         (const void *)&norm_kernel<WPR, P, true, 2, NT>, (const void *)&norm_kernel<WPR, P, true, 3, NT>}};
+    return out == kOutPlainInt8 ? (const void *)&norm_kernel<WPR, P, false, 4, NT> : fn[res][out];
 }
 
 template <int WPR, int P>
@@ -402,12 +427,12 @@ const void *norm_fn(bool res, int out, bool nt)
 const void *norm_any_fn(bool res, int out)
 {
     using namespace skg;
-    static const void *const fn[2][3] = {
+    static const void *const fn[2][4] = {
         {(const void *)&norm_any_kernel<false, 0>, (const void *)&norm_any_kernel<false, 1>,
-         (const void *)&norm_any_kernel<false, 2>},
+         (const void *)&norm_any_kernel<false, 2>, (const void *)&norm_any_kernel<false, 3>},
         {(const void *)&norm_any_kernel<true, 0>, (const void *)&norm_any_kernel<true, 1>,
-         (const void *)&norm_any_kernel<true, 2>}};
-    return fn[res][out];
+         (const void *)&norm_any_kernel<true, 2>, (const void *)&norm_any_kernel<true, 3>}};
+    return out == kOutPlainInt8 ? (const void *)&norm_any_kernel<false, 4> : fn[res][out];
 }
 
 // One block per unit of rows, over two dimensions: a launch holds fewer than 2^32 threads
@@ -418,22 +443,22 @@ dim3 row_grid(int64_t blocks)
     return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
 }
 
-int run_norm(const skinny_norm_t *n, bool fp8, hipStream_t stream)
+// A call whose arguments have been checked with the result st.
+int run_norm(const skinny_norm_t *n, int st, int out, hipStream_t stream)
 {
-    int st = validate_norm(n, fp8);
     if (st != SKINNY_OK || n->M == 0 || n->D == 0)
         return st;
+    const bool bytes = out != skg::kOutBf16;
     int cus = 0;
     st = ops_device(&cus);
     if (st != SKINNY_OK)
         return st;
     skg::NormArgs a{static_cast<const uint16_t *>(n->x), static_cast<const uint16_t *>(n->residual),
                     static_cast<const uint16_t *>(n->weight), static_cast<uint16_t *>(n->residual_out), n->y,
-                    fp8 ? n->scale : nullptr, n->ldx, n->ldr, n->ldro, n->ldy, n->M, n->D,
+                    bytes ? n->scale : nullptr, n->ldx, n->ldr, n->ldro, n->ldy, n->M, n->D,
                     n->group ? (n->D + 127) / 128 : 1, n->eps};
     void *args[] = {&a};
     const bool res = n->residual != nullptr;
-    const int out = !fp8 ? skg::kOutBf16 : n->group ? skg::kOutGroup : skg::kOutRow;
     if (n->D > 32768)
         return ops_launch(norm_any_fn(res, out), row_grid(n->M), 256, args, stream);
     const void *fn;
@@ -442,8 +467,8 @@ int run_norm(const skinny_norm_t *n, bool fp8, hipStream_t stream)
     // Beyond the 256 MB that the device's last cache holds, nothing read or written is
     // there for the next kernel: 8192 x 4096 with residual to e4m3 38.9 us with the
     // non-temporal hint on everything, 42.5 without.
-    const int64_t bytes = (int64_t)n->M * D * ((res ? 6 : 2) + (fp8 ? 1 : 2));
-    const bool nt = bytes > (INT64_C(192) << 20);
+    const int64_t moved = (int64_t)n->M * D * ((res ? 6 : 2) + (bytes ? 1 : 2));
+    const bool nt = moved > (INT64_C(192) << 20);
     if (D <= 8192 && n->M <= 1024) {
         // few rows: one piece a lane and more waves a row; M = 64 x 4096 3.0 us against 3.5,
         // 512 4.8 against 5, 2048 11.5 against 11.1. At most 1024 x 8192 x 8 bytes: never nt
@@ -513,12 +538,23 @@ extern "C" {
 
 int skinny_rms_norm_bf16(const skinny_norm_t *args, hipStream_t stream)
 {
-    return skg_host::run_norm(args, false, stream);
+    return skg_host::run_norm(args, skg_host::validate_norm(args, false), skg::kOutBf16, stream);
 }
 
 int skinny_rms_norm_fp8(const skinny_norm_t *args, hipStream_t stream)
 {
-    return skg_host::run_norm(args, true, stream);
+    const int st = skg_host::validate_norm(args, true);
+    return skg_host::run_norm(args, st, st == SKINNY_OK && args->group ? skg::kOutGroup : skg::kOutRow, stream);
+}
+
+int skinny_rms_norm_int8(const skinny_norm_t *args, hipStream_t stream)
+{
+    return skg_host::run_norm(args, skg_host::validate_norm_int8(args), skg::kOutInt8, stream);
+}
+
+int skinny_quantize_int8(const skinny_norm_t *args, hipStream_t stream)
+{
+    return skg_host::run_norm(args, skg_host::validate_quantize(args), skg::kOutPlainInt8, stream);
 }
 
 }  // extern "C"

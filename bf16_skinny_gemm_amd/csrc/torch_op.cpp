@@ -139,19 +139,23 @@ c10::SmallVector<int64_t, 6> with_last(const at::Tensor &x, int64_t last)
     return shape;
 }
 
-// group < 0: bfloat16 output; else e4m3 with scales. Outputs: y, scale, new residual
-// (undefined where there is none).
+// What a norm's call gives: bfloat16, e4m3 with scales per row or per 128 columns, 8-bit
+// integers with scales per row of the norm, or of x itself (no weight).
+enum class Out { bf16, rows, groups, int8, plain_int8 };
+
+// Outputs: y, scale, new residual (undefined where there is none).
 std::tuple<at::Tensor, at::Tensor, at::Tensor> norm_gpu(const char *op, const at::Tensor &x,
-                                                        const at::Tensor *residual, const at::Tensor &weight,
-                                                        double eps, int64_t group)
+                                                        const at::Tensor *residual, const at::Tensor *weight,
+                                                        double eps, Out out)
 {
     check_matrix(op, x, at::kBFloat16);
-    check_gpu(op, x, weight, "weight", at::kBFloat16);
     const int64_t D = x.size(-1);
     TORCH_CHECK_VALUE(D > 0, op, ": the width must be above 0");
-    TORCH_CHECK_VALUE(weight.dim() == 1 && weight.size(0) == D && weight.is_contiguous(), op,
-                      ": weight must be a contiguous [", D, "], got ", weight.sizes());
-    TORCH_CHECK_VALUE(group < 0 || group == 0 || group == 128, op, ": group must be 0 (per row) or 128, got ", group);
+    if (weight) {
+        check_gpu(op, x, *weight, "weight", at::kBFloat16);
+        TORCH_CHECK_VALUE(weight->dim() == 1 && weight->size(0) == D && weight->is_contiguous(), op,
+                          ": weight must be a contiguous [", D, "], got ", weight->sizes());
+    }
     if (residual) {
         check_gpu(op, x, *residual, "residual", at::kBFloat16);
         TORCH_CHECK_VALUE(residual->sizes() == x.sizes(), op, ": residual must have x's shape ", x.sizes(), ", got ",
@@ -161,8 +165,10 @@ std::tuple<at::Tensor, at::Tensor, at::Tensor> norm_gpu(const char *op, const at
     const Rows xr = rows_of(x, D);
     Rows rr{};
     at::Tensor h, scale;
-    const bool fp8 = group >= 0;
-    at::Tensor y = output(x.sizes(), fp8 ? at::kFloat8_e4m3fn : at::kBFloat16, x);
+    const at::ScalarType type = out == Out::bf16                       ? at::kBFloat16
+                                : out == Out::rows || out == Out::groups ? at::kFloat8_e4m3fn
+                                                                       : at::kChar;
+    at::Tensor y = output(x.sizes(), type, x);
     skinny_norm_t n{};
     n.x = xr.p;
     n.ldx = xr.ld;
@@ -174,42 +180,51 @@ std::tuple<at::Tensor, at::Tensor, at::Tensor> norm_gpu(const char *op, const at
         n.residual_out = h.data_ptr();
         n.ldro = D;
     }
-    n.weight = weight.data_ptr();
+    n.weight = weight ? weight->data_ptr() : nullptr;
     n.y = y.data_ptr();
     n.ldy = D;
     n.M = size32(op, xr.M, "the number of rows");
     n.D = size32(op, D, "the width");
     n.eps = (float)eps;
-    if (fp8) {
+    if (out != Out::bf16) {
         c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end() - 1);
-        if (group)
-            shape.push_back((D + group - 1) / group);
+        n.group = out == Out::groups ? 128 : 0;
+        if (n.group)
+            shape.push_back((D + n.group - 1) / n.group);
         scale = output(shape, at::kFloat, x);
         n.scale = scale.data_ptr<float>();
-        n.group = (int32_t)group;
     }
     const hipStream_t stream = c10::hip::getCurrentHIPStream(x.device().index()).stream();
-    check_status(op, fp8 ? skinny_rms_norm_fp8(&n, stream) : skinny_rms_norm_bf16(&n, stream));
+    check_status(op, out == Out::bf16         ? skinny_rms_norm_bf16(&n, stream)
+                     : out == Out::int8       ? skinny_rms_norm_int8(&n, stream)
+                     : out == Out::plain_int8 ? skinny_quantize_int8(&n, stream)
+                                              : skinny_rms_norm_fp8(&n, stream));
     return {y, scale, h};
+}
+
+Out fp8_out(const char *op, int64_t group)
+{
+    TORCH_CHECK_VALUE(group == 0 || group == 128, op, ": group must be 0 (per row) or 128, got ", group);
+    return group ? Out::groups : Out::rows;
 }
 
 at::Tensor rms_norm_gpu(const at::Tensor &x, const at::Tensor &weight, double eps)
 {
-    return std::get<0>(norm_gpu("skinny::rms_norm", x, nullptr, weight, eps, -1));
+    return std::get<0>(norm_gpu("skinny::rms_norm", x, nullptr, &weight, eps, Out::bf16));
 }
 
 std::tuple<at::Tensor, at::Tensor> add_rms_norm_gpu(const at::Tensor &x, const at::Tensor &residual,
                                                     const at::Tensor &weight, double eps)
 {
-    auto r = norm_gpu("skinny::add_rms_norm", x, &residual, weight, eps, -1);
+    auto r = norm_gpu("skinny::add_rms_norm", x, &residual, &weight, eps, Out::bf16);
     return {std::get<0>(r), std::get<2>(r)};
 }
 
 std::tuple<at::Tensor, at::Tensor> rms_norm_fp8_gpu(const at::Tensor &x, const at::Tensor &weight, double eps,
                                                     int64_t group)
 {
-    TORCH_CHECK_VALUE(group >= 0, "skinny::rms_norm_fp8: group must be 0 (per row) or 128, got ", group);
-    auto r = norm_gpu("skinny::rms_norm_fp8", x, nullptr, weight, eps, group);
+    const char *op = "skinny::rms_norm_fp8";
+    auto r = norm_gpu(op, x, nullptr, &weight, eps, fp8_out(op, group));
     return {std::get<0>(r), std::get<1>(r)};
 }
 
@@ -217,8 +232,26 @@ std::tuple<at::Tensor, at::Tensor, at::Tensor> add_rms_norm_fp8_gpu(const at::Te
                                                                     const at::Tensor &weight, double eps,
                                                                     int64_t group)
 {
-    TORCH_CHECK_VALUE(group >= 0, "skinny::add_rms_norm_fp8: group must be 0 (per row) or 128, got ", group);
-    return norm_gpu("skinny::add_rms_norm_fp8", x, &residual, weight, eps, group);
+    const char *op = "skinny::add_rms_norm_fp8";
+    return norm_gpu(op, x, &residual, &weight, eps, fp8_out(op, group));
+}
+
+std::tuple<at::Tensor, at::Tensor> quantize_int8_gpu(const at::Tensor &x)
+{
+    auto r = norm_gpu("skinny::quantize_int8", x, nullptr, nullptr, 0.0, Out::plain_int8);
+    return {std::get<0>(r), std::get<1>(r)};
+}
+
+std::tuple<at::Tensor, at::Tensor> rms_norm_int8_gpu(const at::Tensor &x, const at::Tensor &weight, double eps)
+{
+    auto r = norm_gpu("skinny::rms_norm_int8", x, nullptr, &weight, eps, Out::int8);
+    return {std::get<0>(r), std::get<1>(r)};
+}
+
+std::tuple<at::Tensor, at::Tensor, at::Tensor> add_rms_norm_int8_gpu(const at::Tensor &x, const at::Tensor &residual,
+                                                                     const at::Tensor &weight, double eps)
+{
+    return norm_gpu("skinny::add_rms_norm_int8", x, &residual, &weight, eps, Out::int8);
 }
 
 using Opt = std::optional<at::Tensor>;
@@ -264,10 +297,9 @@ void check_scales(const char *op, const at::Tensor &x, const at::Tensor &xs, con
     }
 }
 
-at::Tensor linear_any(const char *op, const at::Tensor &x, const at::Tensor *xs, const Side *sides, int mats,
-                      const Opt &residual, c10::string_view act, bool out_f32)
+at::Tensor linear_any(const char *op, at::ScalarType type, const at::Tensor &x, const at::Tensor *xs,
+                      const Side *sides, int mats, const Opt &residual, c10::string_view act, bool out_f32)
 {
-    const at::ScalarType type = xs ? at::kFloat8_e4m3fn : at::kBFloat16;
     check_matrix(op, x, type);
     const int64_t K = x.size(-1);
     const at::Tensor &w0 = sides[0].w;
@@ -289,7 +321,7 @@ at::Tensor linear_any(const char *op, const at::Tensor &x, const at::Tensor *xs,
                           ": weights must be contiguous [", N, ", ", K, "], got ", s.w.sizes());
         (i ? a.W1 : a.W0) = s.w.data_ptr();
         if (xs) {
-            const bool blocks = sides[0].scale->dim() == 2;
+            const bool blocks = type == at::kFloat8_e4m3fn && sides[0].scale->dim() == 2;
             check_scales(op, x, *xs, *s.scale, xr.M, N, K, blocks);
             a.scales = blocks ? SKINNY_SCALES_BLOCK : SKINNY_SCALES_ROW;
             a.x_scale = xs->data_ptr<float>();
@@ -318,7 +350,9 @@ at::Tensor linear_any(const char *op, const at::Tensor &x, const at::Tensor *xs,
     a.ldy = N;
     a.out_f32 = out_f32;
     const hipStream_t stream = c10::hip::getCurrentHIPStream(x.device().index()).stream();
-    check_status(op, xs ? skinny_linear_fp8(&a, stream) : skinny_linear_bf16(&a, stream));
+    check_status(op, type == at::kBFloat16 ? skinny_linear_bf16(&a, stream)
+                     : type == at::kChar   ? skinny_linear_int8(&a, stream)
+                                           : skinny_linear_fp8(&a, stream));
     return y;
 }
 
@@ -326,14 +360,14 @@ at::Tensor linear_act_gpu(const at::Tensor &x, const at::Tensor &weight, const O
                           c10::string_view act, bool out_f32)
 {
     const Side s[] = {{weight, nullptr, bias}};
-    return linear_any("skinny::linear_act", x, nullptr, s, 1, residual, act, out_f32);
+    return linear_any("skinny::linear_act", at::kBFloat16, x, nullptr, s, 1, residual, act, out_f32);
 }
 
 at::Tensor linear_gated_gpu(const at::Tensor &x, const at::Tensor &w_gate, const at::Tensor &w_up, const Opt &b_gate,
                             const Opt &b_up, c10::string_view act, bool out_f32)
 {
     const Side s[] = {{w_gate, nullptr, b_gate}, {w_up, nullptr, b_up}};
-    return linear_any("skinny::linear_gated", x, nullptr, s, 2, std::nullopt, act, out_f32);
+    return linear_any("skinny::linear_gated", at::kBFloat16, x, nullptr, s, 2, std::nullopt, act, out_f32);
 }
 
 at::Tensor linear_fp8_gpu(const at::Tensor &x, const at::Tensor &x_scale, const at::Tensor &weight,
@@ -341,7 +375,7 @@ at::Tensor linear_fp8_gpu(const at::Tensor &x, const at::Tensor &x_scale, const 
                           bool out_f32)
 {
     const Side s[] = {{weight, &w_scale, bias}};
-    return linear_any("skinny::linear_fp8", x, &x_scale, s, 1, residual, act, out_f32);
+    return linear_any("skinny::linear_fp8", at::kFloat8_e4m3fn, x, &x_scale, s, 1, residual, act, out_f32);
 }
 
 at::Tensor linear_gated_fp8_gpu(const at::Tensor &x, const at::Tensor &x_scale, const at::Tensor &w_gate,
@@ -349,7 +383,23 @@ at::Tensor linear_gated_fp8_gpu(const at::Tensor &x, const at::Tensor &x_scale, 
                                 const Opt &b_gate, const Opt &b_up, c10::string_view act, bool out_f32)
 {
     const Side s[] = {{w_gate, &gate_scale, b_gate}, {w_up, &up_scale, b_up}};
-    return linear_any("skinny::linear_gated_fp8", x, &x_scale, s, 2, std::nullopt, act, out_f32);
+    return linear_any("skinny::linear_gated_fp8", at::kFloat8_e4m3fn, x, &x_scale, s, 2, std::nullopt, act, out_f32);
+}
+
+at::Tensor linear_int8_gpu(const at::Tensor &x, const at::Tensor &x_scale, const at::Tensor &weight,
+                           const at::Tensor &w_scale, const Opt &bias, const Opt &residual, c10::string_view act,
+                           bool out_f32)
+{
+    const Side s[] = {{weight, &w_scale, bias}};
+    return linear_any("skinny::linear_int8", at::kChar, x, &x_scale, s, 1, residual, act, out_f32);
+}
+
+at::Tensor linear_gated_int8_gpu(const at::Tensor &x, const at::Tensor &x_scale, const at::Tensor &w_gate,
+                                 const at::Tensor &gate_scale, const at::Tensor &w_up, const at::Tensor &up_scale,
+                                 const Opt &b_gate, const Opt &b_up, c10::string_view act, bool out_f32)
+{
+    const Side s[] = {{w_gate, &gate_scale, b_gate}, {w_up, &up_scale, b_up}};
+    return linear_any("skinny::linear_gated_int8", at::kChar, x, &x_scale, s, 2, std::nullopt, act, out_f32);
 }
 
 // CPU tensors: every operator refuses them by name.
@@ -377,6 +427,13 @@ TORCH_LIBRARY(skinny, m)
           "Tensor? residual=None, str act='none', bool out_f32=False) -> Tensor");
     m.def("linear_gated_fp8(Tensor x, Tensor x_scale, Tensor w_gate, Tensor gate_scale, Tensor w_up, "
           "Tensor up_scale, Tensor? b_gate=None, Tensor? b_up=None, str act='silu', bool out_f32=False) -> Tensor");
+    m.def("quantize_int8(Tensor x) -> (Tensor, Tensor)");
+    m.def("rms_norm_int8(Tensor x, Tensor weight, float eps) -> (Tensor, Tensor)");
+    m.def("add_rms_norm_int8(Tensor x, Tensor residual, Tensor weight, float eps) -> (Tensor, Tensor, Tensor)");
+    m.def("linear_int8(Tensor x, Tensor x_scale, Tensor weight, Tensor w_scale, Tensor? bias=None, "
+          "Tensor? residual=None, str act='none', bool out_f32=False) -> Tensor");
+    m.def("linear_gated_int8(Tensor x, Tensor x_scale, Tensor w_gate, Tensor gate_scale, Tensor w_up, "
+          "Tensor up_scale, Tensor? b_gate=None, Tensor? b_up=None, str act='silu', bool out_f32=False) -> Tensor");
 }
 
 TORCH_LIBRARY_IMPL(skinny, CUDA, m)
@@ -390,12 +447,18 @@ TORCH_LIBRARY_IMPL(skinny, CUDA, m)
     m.impl("linear_gated", &linear_gated_gpu);
     m.impl("linear_fp8", &linear_fp8_gpu);
     m.impl("linear_gated_fp8", &linear_gated_fp8_gpu);
+    m.impl("quantize_int8", &quantize_int8_gpu);
+    m.impl("rms_norm_int8", &rms_norm_int8_gpu);
+    m.impl("add_rms_norm_int8", &add_rms_norm_int8_gpu);
+    m.impl("linear_int8", &linear_int8_gpu);
+    m.impl("linear_gated_int8", &linear_gated_int8_gpu);
 }
 
 TORCH_LIBRARY_IMPL(skinny, CPU, m)
 {
     m.impl("linear", &linear_cpu);
     for (const char *op : {"rms_norm", "add_rms_norm", "rms_norm_fp8", "add_rms_norm_fp8", "linear_act",
-                           "linear_gated", "linear_fp8", "linear_gated_fp8"})
+                           "linear_gated", "linear_fp8", "linear_gated_fp8", "quantize_int8", "rms_norm_int8",
+                           "add_rms_norm_int8", "linear_int8", "linear_gated_int8"})
         m.impl(op, torch::CppFunction::makeFromBoxedFunction<&refuse_cpu>());
 }

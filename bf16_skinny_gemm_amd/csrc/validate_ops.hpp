@@ -162,6 +162,33 @@ inline int validate_linear(const skinny_linear_t *a, bool fp8)
     return SKINNY_OK;
 }
 
+// Products of K 8-bit integers, each at most 2^14 in magnitude, must add up within 32 bits.
+constexpr int32_t kMaxInt8Depth = 131071;
+
+inline int validate_linear_int8(const skinny_linear_t *a)
+{
+    if (!a || a->scales != SKINNY_SCALES_ROW || a->K > kMaxInt8Depth)
+        return SKINNY_ERR_INVALID_ARG;
+    return validate_linear(a, true);
+}
+
+inline int validate_norm_int8(const skinny_norm_t *a)
+{
+    if (!a || a->group != 0)
+        return SKINNY_ERR_INVALID_ARG;
+    return validate_norm(a, true);
+}
+
+// skinny_quantize_int8: a norm's call without weight, residual and eps.
+inline int validate_quantize(const skinny_norm_t *a)
+{
+    if (!a || a->weight || a->residual || a->residual_out || a->eps != 0.0f)
+        return SKINNY_ERR_INVALID_ARG;
+    skinny_norm_t with = *a;
+    with.weight = a->x;  // its extent is a part of x's
+    return validate_norm_int8(&with);
+}
+
 // Rows of x and W can be read in 16-byte pieces, and the 32-bit byte offsets of the
 // kernels' buffer resources reach: 256 rows of x or W from a tile's first.
 inline bool linear_vector_ok(const skinny_linear_t &a, bool fp8)

@@ -18,8 +18,8 @@ linear path otherwise. Here:
   ``torch.nn.functional.linear`` only when ``fallback=True`` (the default for the
   module hook), else they raise;
 * :func:`install` swaps the forward of ``nn.Linear`` modules for the routed one;
-* ``rms_norm``, ``add_rms_norm``, ``rms_norm_fp8``, ``add_rms_norm_fp8``, ``linear_act``,
-  ``linear_gated``, ``linear_fp8`` and ``linear_gated_fp8`` (``torch.ops.skinny.*``, same
+* ``rms_norm``, ``add_rms_norm``, ``linear_act`` and ``linear_gated``, their 8-bit forms with
+  ``_fp8`` and ``_int8`` behind the name, and ``quantize_int8`` (``torch.ops.skinny.*``, same
   registration) are the operators around the projection, for any number of rows;
   :func:`install` with ``fused=True`` routes biased ``nn.Linear`` layers and
   ``nn.RMSNorm`` modules to them.
@@ -43,6 +43,7 @@ from torch.overrides import TorchFunctionMode
 
 from . import _on_device, _stream_handle, lib, skinny_gemm_bf16
 from . import linear as _linear_call
+from . import quantize_int8 as _quantize_call
 from . import rms_norm as _norm_call
 from .build import TORCH_OP_PATH
 
@@ -145,6 +146,14 @@ _SCHEMAS = (
     "linear_gated_fp8(Tensor x, Tensor x_scale, Tensor w_gate, Tensor gate_scale, Tensor w_up, "
     "Tensor up_scale, Tensor? b_gate=None, Tensor? b_up=None, str act='silu', "
     "bool out_f32=False) -> Tensor",
+    "quantize_int8(Tensor x) -> (Tensor, Tensor)",
+    "rms_norm_int8(Tensor x, Tensor weight, float eps) -> (Tensor, Tensor)",
+    "add_rms_norm_int8(Tensor x, Tensor residual, Tensor weight, float eps) -> (Tensor, Tensor, Tensor)",
+    "linear_int8(Tensor x, Tensor x_scale, Tensor weight, Tensor w_scale, Tensor? bias=None, "
+    "Tensor? residual=None, str act='none', bool out_f32=False) -> Tensor",
+    "linear_gated_int8(Tensor x, Tensor x_scale, Tensor w_gate, Tensor gate_scale, Tensor w_up, "
+    "Tensor up_scale, Tensor? b_gate=None, Tensor? b_up=None, str act='silu', "
+    "bool out_f32=False) -> Tensor",
 )
 
 
@@ -167,6 +176,11 @@ def _norm_py(x, weight, eps, residual=None, quant=None):
     shapes = [x.shape] + ([_scale_shape(x, quant == "group")] if quant else []) + [x.shape]
     got = tuple(g.reshape(s) for g, s in zip(got, shapes))
     return got[0] if len(got) == 1 else got
+
+
+def _quantize_py(x):
+    q, scale = _quantize_call(x.reshape(-1, x.shape[-1]))
+    return q.reshape(x.shape), scale.reshape(x.shape[:-1])
 
 
 def _linear_py(x, weight, bias, residual, act, out_f32, W_up=None, bias_up=None, x_scale=None,
@@ -194,7 +208,20 @@ _PY_KERNELS = {
         x, w, b, r, act, f32, x_scale=xs, w_scale=ws),
     "linear_gated_fp8": lambda x, xs, w, ws, u, us, b=None, bu=None, act="silu", f32=False: _linear_py(
         x, w, b, None, act, f32, u, bu, xs, ws, us),
+    "quantize_int8": _quantize_py,
+    "rms_norm_int8": lambda x, w, eps: _norm_py(x, w, eps, None, "int8"),
+    "add_rms_norm_int8": lambda x, r, w, eps: _norm_py(x, w, eps, r, "int8"),
+    "linear_int8": lambda x, xs, w, ws, b=None, r=None, act="none", f32=False: _linear_py(
+        _int8(x), w, b, r, act, f32, x_scale=xs, w_scale=ws),
+    "linear_gated_int8": lambda x, xs, w, ws, u, us, b=None, bu=None, act="silu", f32=False: _linear_py(
+        _int8(x), w, b, None, act, f32, u, bu, xs, ws, us),
 }
+
+
+def _int8(x):
+    if x.dtype != torch.int8:
+        raise ValueError(f"x must be int8, got {x.dtype}")
+    return x
 
 
 def _refuse_cpu(name):
@@ -213,6 +240,10 @@ def _q_fake(x, group):
             x.new_empty(_scale_shape(x, group), dtype=torch.float32))
 
 
+def _q8_fake(x):
+    return x.new_empty(x.shape, dtype=torch.int8), x.new_empty(x.shape[:-1], dtype=torch.float32)
+
+
 _FAKES = {
     "rms_norm": lambda x, weight, eps: x.new_empty(x.shape),
     "add_rms_norm": lambda x, residual, weight, eps: (x.new_empty(x.shape), x.new_empty(x.shape)),
@@ -225,6 +256,13 @@ _FAKES = {
     "linear_fp8": lambda x, x_scale, weight, w_scale, bias=None, residual=None, act="none",
     out_f32=False: _y_fake(x, weight.shape[0], out_f32),
     "linear_gated_fp8": lambda x, x_scale, w_gate, gate_scale, w_up, up_scale, b_gate=None, b_up=None,
+    act="silu", out_f32=False: _y_fake(x, w_gate.shape[0], out_f32),
+    "quantize_int8": lambda x: _q8_fake(x),
+    "rms_norm_int8": lambda x, weight, eps: _q8_fake(x),
+    "add_rms_norm_int8": lambda x, residual, weight, eps: (*_q8_fake(x), x.new_empty(x.shape)),
+    "linear_int8": lambda x, x_scale, weight, w_scale, bias=None, residual=None, act="none",
+    out_f32=False: _y_fake(x, weight.shape[0], out_f32),
+    "linear_gated_int8": lambda x, x_scale, w_gate, gate_scale, w_up, up_scale, b_gate=None, b_up=None,
     act="silu", out_f32=False: _y_fake(x, w_gate.shape[0], out_f32),
 }
 
@@ -243,6 +281,11 @@ linear_act = torch.ops.skinny.linear_act.default
 linear_gated = torch.ops.skinny.linear_gated.default
 linear_fp8 = torch.ops.skinny.linear_fp8.default
 linear_gated_fp8 = torch.ops.skinny.linear_gated_fp8.default
+quantize_int8 = torch.ops.skinny.quantize_int8.default
+rms_norm_int8 = torch.ops.skinny.rms_norm_int8.default
+add_rms_norm_int8 = torch.ops.skinny.add_rms_norm_int8.default
+linear_int8 = torch.ops.skinny.linear_int8.default
+linear_gated_int8 = torch.ops.skinny.linear_gated_int8.default
 
 
 _func_level = torch._C._functorch.maybe_current_level
@@ -382,4 +425,5 @@ def install(module: torch.nn.Module, fallback: bool = True, fused: bool = False)
 
 __all__ = ["linear", "skinny_linear", "install", "qualifies", "qualifies_fused", "CPP_OP", "FUSED_ROWS",
            "rms_norm", "add_rms_norm", "rms_norm_fp8", "add_rms_norm_fp8", "linear_act", "linear_gated",
-           "linear_fp8", "linear_gated_fp8"]
+           "linear_fp8", "linear_gated_fp8", "quantize_int8", "rms_norm_int8", "add_rms_norm_int8",
+           "linear_int8", "linear_gated_int8"]

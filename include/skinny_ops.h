@@ -2,7 +2,7 @@
  * skinny_ops.h -- C ABI of the operators around the skinny GEMM, in the same library
  * (libskinny_gemm_bf16.so): the norm in front of a projection, and projections whose
  * bias, activation, gate and residual are applied before the result is stored, on
- * bfloat16 or on 8-bit floats with scales.
+ * bfloat16, or on 8-bit floats or integers with scales.
  *
  * Conventions shared by every entry point below:
  *  - Pointers are DEVICE pointers. bfloat16 and e4m3 values (the OCP 8-bit float
@@ -55,12 +55,12 @@ typedef struct skinny_norm {
     const void *residual;     /* [M][D] bfloat16, row stride ldr, or NULL */
     const void *weight;       /* [D] bfloat16 */
     void *residual_out;       /* [M][D] bfloat16, row stride ldro, or NULL */
-    void *y;                  /* [M][D] bfloat16, or e4m3 for skinny_rms_norm_fp8; stride ldy */
-    float *scale;             /* skinny_rms_norm_fp8 only: [M] or [M][ceil(D / group)] */
+    void *y;                  /* [M][D] bfloat16, or e4m3 for skinny_rms_norm_fp8, or int8; stride ldy */
+    float *scale;             /* 8-bit outputs only: [M] or [M][ceil(D / group)] */
     int64_t ldx, ldr, ldro, ldy;
     int32_t M, D;
     int32_t group;            /* skinny_rms_norm_fp8: 0 = one scale per row, 128 = one per
-                                 128 columns; skinny_rms_norm_bf16: 0 */
+                                 128 columns; the others: 0 */
     float eps;
 } skinny_norm_t;
 
@@ -73,6 +73,17 @@ int skinny_rms_norm_bf16(const skinny_norm_t *args, hipStream_t stream);
  * and groups of zeros give zeros (with eps == 0 a row of zeros is 0 / 0: NaN). A NaN in a row makes the row's scales and values NaN. An infinity makes
  * the scale of its row or group NaN with all its values, and the row's other groups 0. */
 int skinny_rms_norm_fp8(const skinny_norm_t *args, hipStream_t stream);
+
+/* y as 8-bit integers with a float32 scale per row (group 0): scale = max(largest |y|, 2^-100)
+ * / 127 and q = y / scale rounded to the nearest integer, ties to even, with the quotient as
+ * above, so -127 .. 127. Rows of zeros give zeros; a NaN or an infinity in a row makes its
+ * scale NaN and its q 0, so that q * scale is NaN. */
+int skinny_rms_norm_int8(const skinny_norm_t *args, hipStream_t stream);
+
+/* The rows of x themselves as 8-bit integers: y = x in the formulas of skinny_rms_norm_int8.
+ * weight, residual and residual_out are NULL, eps and group 0. An infinity makes the scale
+ * of its row infinite and its q 0. */
+int skinny_quantize_int8(const skinny_norm_t *args, hipStream_t stream);
 
 /* ---- Projections with an epilogue ----------------------------------------------
  *   z[m, n] = sum_k x[m, k] * W0[n, k] + bias0[n]
@@ -103,7 +114,7 @@ typedef enum skinny_scales {
 typedef struct skinny_linear {
     const void *x;            /* [M][K], row stride ldx >= K */
     const void *W0, *W1;      /* [N][K] contiguous; W1 NULL: not gated */
-    const float *x_scale;     /* skinny_linear_fp8 only, contiguous float32 (see skinny_scales) */
+    const float *x_scale;     /* 8-bit x and W only, contiguous float32 (see skinny_scales) */
     const float *w0_scale, *w1_scale;
     const void *bias0, *bias1; /* [N] bfloat16 or NULL; bias1 only with W1 */
     const void *residual;     /* [M][N] bfloat16, row stride ldr >= N, or NULL */
@@ -112,7 +123,7 @@ typedef struct skinny_linear {
     int32_t M, N, K;
     int32_t act;              /* skinny_act_t */
     int32_t out_f32;          /* 0 or 1 */
-    int32_t scales;           /* skinny_linear_fp8: skinny_scales_t; skinny_linear_bf16: 0 */
+    int32_t scales;           /* skinny_linear_fp8, _int8: skinny_scales_t; skinny_linear_bf16: 0 */
 } skinny_linear_t;
 
 /* x and W bfloat16. */
@@ -126,6 +137,13 @@ int skinny_linear_bf16(const skinny_linear_t *args, hipStream_t stream);
  * columns off (towards zero) at 2^-13 of the largest before it adds them: about 2e-5 of a
  * result's norm, below bfloat16's rounding of 4e-3. */
 int skinny_linear_fp8(const skinny_linear_t *args, hipStream_t stream);
+
+/* x and W 8-bit integers (two's complement) with one float32 scale per row of x and per row of
+ * W (scales: SKINNY_SCALES_ROW): what skinny_rms_norm_int8 and skinny_quantize_int8 make, and
+ * weights with a scale for each output. The products are added up in 32-bit integers, which is
+ * exact whatever kernel a call takes, so K is at most 131071; the sum is rounded to float32
+ * once and multiplied by the scales. */
+int skinny_linear_int8(const skinny_linear_t *args, hipStream_t stream);
 
 /* The kernel that a projection call takes. Calls with the same element type, scales, gate,
  * output type and class of rows (up to 8, up to 16, more) choose among the same `count`
@@ -149,6 +167,9 @@ typedef struct skinny_linear_plan {
  * touches no device and follows no pointer. SKINNY_ERR_INVALID_ARG for a call without
  * outputs. */
 int skinny_linear_default_plan(const skinny_linear_t *args, int32_t compute_units, skinny_linear_plan_t *out);
+
+/* The same of skinny_linear_int8(args). */
+int skinny_linear_int8_default_plan(const skinny_linear_t *args, int32_t compute_units, skinny_linear_plan_t *out);
 
 #ifdef __cplusplus
 }
