@@ -19,12 +19,12 @@ Python ints; a non-zero status raises :class:`SkinnyError`):
     skinny_gemm_split_k_get_variant, skinny_gemm_split_k_default_plan,
     skinny_rms_norm_bf16, skinny_rms_norm_fp8, skinny_linear_bf16, skinny_linear_fp8,
     skinny_linear_default_plan, skinny_rms_norm_int8, skinny_quantize_int8, skinny_linear_int8,
-    skinny_linear_int8_default_plan
+    skinny_linear_int8_default_plan, skinny_route, skinny_experts_workspace_bytes, skinny_experts
 
 Tensor helpers: :func:`gemm`, :func:`gemm_pair`, :func:`gemm_pair_strided`,
 :func:`split_k_workspace`, :func:`gemm_split_k` and :func:`gemm_split_k_noalloc`;
 :func:`rms_norm`, :func:`quantize_int8` and :func:`linear` (any number of rows,
-``include/skinny_ops.h``).
+``include/skinny_ops.h``); :func:`route` and :func:`experts` (``include/skinny_moe.h``).
 """
 from __future__ import annotations
 
@@ -63,6 +63,15 @@ SKINNY_LINEAR_ELEMENTS = 0
 SKINNY_LINEAR_STREAM = 1
 SKINNY_LINEAR_TILE = 2
 
+SKINNY_SCORE_SOFTMAX = 0
+SKINNY_SCORE_SIGMOID = 1
+
+SKINNY_WEIGHTS_BF16 = 0
+SKINNY_WEIGHTS_E4M3_ROW = 1
+SKINNY_WEIGHTS_E4M3_BLOCK = 2
+SKINNY_WEIGHTS_INT8_ROW = 3
+
+SCORES = {"softmax": SKINNY_SCORE_SOFTMAX, "sigmoid": SKINNY_SCORE_SIGMOID}
 ACTS = {"none": SKINNY_ACT_NONE, "relu": SKINNY_ACT_RELU, "gelu": SKINNY_ACT_GELU,
         "gelu_tanh": SKINNY_ACT_GELU_TANH, "silu": SKINNY_ACT_SILU}
 
@@ -138,6 +147,29 @@ class LinearPlan(ctypes.Structure):
         return "LinearPlan(" + ", ".join(f"{k}={v}" for k, v in self.as_dict().items()) + ")"
 
 
+class RouteArgs(ctypes.Structure):
+    """skinny_route_t."""
+
+    _fields_ = [
+        ("logits", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("ids", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p), ("ldl", ctypes.c_int64), ("M", ctypes.c_int32),
+        ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32),
+        ("groups", ctypes.c_int32), ("kept", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class ExpertsArgs(ctypes.Structure):
+    """skinny_experts_t."""
+
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "x", "ids", "weights", "w_gate", "w_up", "w_down", "gate_scale", "up_scale", "down_scale",
+        "residual", "y", "workspace")] + [("workspace_bytes", ctypes.c_size_t)] + [
+        (name, ctypes.c_int64) for name in ("ldx", "ldr", "ldy", "up_stride", "down_stride",
+                                            "up_scale_stride", "down_scale_stride")] + [
+        (name, ctypes.c_int32) for name in ("M", "E", "k", "H", "I", "act", "type")]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -180,9 +212,12 @@ def lib() -> ctypes.CDLL:
         for name, args in (("skinny_rms_norm_bf16", NormArgs), ("skinny_rms_norm_fp8", NormArgs),
                            ("skinny_rms_norm_int8", NormArgs), ("skinny_quantize_int8", NormArgs),
                            ("skinny_linear_bf16", LinearArgs), ("skinny_linear_fp8", LinearArgs),
-                           ("skinny_linear_int8", LinearArgs)):
+                           ("skinny_linear_int8", LinearArgs), ("skinny_route", RouteArgs),
+                           ("skinny_experts", ExpertsArgs)):
             getattr(L, name).argtypes = [ctypes.POINTER(args), vp]
             getattr(L, name).restype = ctypes.c_int
+        L.skinny_experts_workspace_bytes.argtypes = [ctypes.c_int32] * 4
+        L.skinny_experts_workspace_bytes.restype = ctypes.c_size_t
         for name in ("skinny_linear_default_plan", "skinny_linear_int8_default_plan"):
             getattr(L, name).argtypes = [ctypes.POINTER(LinearArgs), ctypes.c_int32, ctypes.POINTER(LinearPlan)]
             getattr(L, name).restype = ctypes.c_int
@@ -375,6 +410,19 @@ def skinny_linear_int8_default_plan(args: LinearArgs, compute_units: int = 256) 
     _check(lib().skinny_linear_int8_default_plan(ctypes.byref(args), compute_units, ctypes.byref(p)),
            "skinny_linear_int8_default_plan")
     return p
+
+
+def skinny_route(args: RouteArgs, stream: int = 0) -> None:
+    _check(lib().skinny_route(ctypes.byref(args), stream), "skinny_route")
+
+
+def skinny_experts_workspace_bytes(M: int, k: int, E: int, I: int) -> int:
+    """Workspace bytes of an experts call (0: no call with these sizes is accepted, or M is 0)."""
+    return int(lib().skinny_experts_workspace_bytes(M, k, E, I))
+
+
+def skinny_experts(args: ExpertsArgs, stream: int = 0) -> None:
+    _check(lib().skinny_experts(ctypes.byref(args), stream), "skinny_experts")
 
 
 # ---- tensor helpers ---------------------------------------------------------
@@ -777,6 +825,138 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None,
     return out
 
 
+def route(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.Tensor | None = None,
+          groups: int = 1, kept: int = 1, renormalize: bool = True, scale: float = 1.0,
+          out_ids: torch.Tensor | None = None,
+          out_weights: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(ids, weights), int32 and float32 [M, k]: the k best of the experts of float32 logits
+    [M, E] (rows may be strided), best first and equal ones by index, and scale times their
+    scores ("softmax" over the row or "sigmoid"), which renormalize makes sum to 1 before. They
+    are ranked by the logits, or by score + bias where float32 bias [E] is given. groups > 1
+    takes them from `kept` of that many runs of experts only: those of the largest rank, or,
+    with a bias, of the largest sum of two ranks. One kernel launch on the current stream;
+    E at most 1024, k and groups at most 64. out_ids and out_weights may be given."""
+    ldl = _matrix(logits, "logits", torch.float32, None)
+    M, E = logits.shape
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {', '.join(SCORES)}, got {score!r}")
+    if not 1 <= E <= 1024:
+        raise ValueError(f"the number of experts must be 1..1024, got {E}")
+    if not (1 <= groups <= 64 and E % groups == 0 and 1 <= kept <= groups):
+        raise ValueError(f"groups must be 1..64 and divide {E}, and kept 1..groups, got {groups} and {kept}")
+    if not 1 <= k <= min(64, kept * (E // groups)):
+        raise ValueError(f"k must be 1..{min(64, kept * (E // groups))}, got {k}")
+    if out_ids is None:
+        out_ids = torch.empty((M, k), dtype=torch.int32, device=logits.device)
+    if out_weights is None:
+        out_weights = torch.empty((M, k), dtype=torch.float32, device=logits.device)
+    a = RouteArgs(logits=logits.data_ptr(), ldl=ldl, M=M, E=E, k=k, score=SCORES[score], groups=groups, kept=kept,
+                  renormalize=bool(renormalize), scale=scale,
+                  bias=_vector(bias, "bias", torch.float32, logits.device, (E,)),
+                  ids=_vector(out_ids, "out_ids", torch.int32, logits.device, (M, k)),
+                  weights=_vector(out_weights, "out_weights", torch.float32, logits.device, (M, k)))
+    s = _stream_handle(logits.device)
+    with _on_device(logits.device):
+        skinny_route(a, s)
+    return out_ids, out_weights
+
+
+def _stack(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, shape: tuple) -> int:
+    """Check a GPU tensor whose parts t[e] are contiguous and return the stride of e."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.device != device or tuple(t.shape) != tuple(shape) or (shape[0] > 0 and not t[0].is_contiguous()):
+        raise ValueError(f"{name} must be {list(shape)} with contiguous parts on {device}, got {list(t.shape)} of strides "
+                         f"{t.stride()} on {t.device}")
+    return t.stride(0) if shape[0] > 1 else t[0].numel()
+
+
+def experts_workspace(M: int, k: int, E: int, I: int, device: torch.device | str = "cuda") -> torch.Tensor:
+    """A uint8 device buffer big enough for experts calls of up to M rows with these sizes (to
+    reuse in calls that follow one another on one stream)."""
+    nbytes = skinny_experts_workspace_bytes(M, k, E, I)
+    if nbytes == 0:
+        raise SkinnyError(SKINNY_ERR_INVALID_ARG, "skinny_experts_workspace_bytes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w_gate: torch.Tensor,
+            w_up: torch.Tensor, w_down: torch.Tensor, gate_scale: torch.Tensor | None = None,
+            up_scale: torch.Tensor | None = None, down_scale: torch.Tensor | None = None,
+            residual: torch.Tensor | None = None, act: str = "silu", out: torch.Tensor | None = None,
+            workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y[m] = sum_j weights[m, j] * (act(x[m] @ w_gate[e].T) * (x[m] @ w_up[e].T)) @ w_down[e].T
+    + residual[m] with e = ids[m, j], for bfloat16 x [M, H] (rows may be strided), int32 ids and
+    float32 weights [M, k]; an id outside 0..E-1 is left out.
+
+    w_gate and w_up [E, I, H] and w_down [E, H, I] are bfloat16, or int8 with float32 scales per
+    row (gate_scale and up_scale [E, I], down_scale [E, H]), or float8_e4m3fn with those or with
+    scales per 128 x 128 block ([E, ceil(I/128), ceil(H/128)], [E, ceil(H/128), ceil(I/128)]). Parts
+    [e] must be contiguous; the two halves of a merged [E, 2 I, H] weight are taken as views.
+    Two kernel launches for every 128 rows on the current stream; for up to some hundred rows.
+    out (which may be the residual) and workspace (from experts_workspace) may be given."""
+    ldx = _matrix(x, "x", torch.bfloat16, None)
+    M, H = x.shape
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    if not isinstance(w_gate, torch.Tensor) or w_gate.dtype not in (torch.bfloat16, torch.int8, torch.float8_e4m3fn):
+        raise TypeError("w_gate must be a bfloat16, int8 or float8_e4m3fn tensor")
+    if w_gate.dim() != 3:
+        raise ValueError(f"w_gate must be [E, I, H], got {list(w_gate.shape)}")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be an [M, k] tensor")
+    dtype, (E, I, _), k = w_gate.dtype, w_gate.shape, ids.shape[1]
+    if not (1 <= E <= 1024 and 1 <= k <= 32 and H >= 1 and I >= 1):
+        raise ValueError(f"E must be 1..1024, k 1..32, H and I above 0, got {E}, {k}, {H} and {I}")
+    if max(H, I) > 0x7FFFFFFF:
+        raise ValueError(f"H and I must fit in 31 bits, got {H} and {I}")
+    a = ExpertsArgs(x=x.data_ptr(), ldx=ldx, M=M, E=E, k=k, H=H, I=I, act=ACTS[act])
+    a.ids = _vector(ids, "ids", torch.int32, x.device, (M, k))
+    a.weights = _vector(weights, "weights", torch.float32, x.device, (M, k))
+    if weights is None:
+        raise TypeError("weights must be a torch.Tensor")
+    a.up_stride = _stack(w_gate, "w_gate", dtype, x.device, (E, I, H))
+    if _stack(w_up, "w_up", dtype, x.device, (E, I, H)) != a.up_stride:
+        raise ValueError("w_gate and w_up must have the same strides")
+    a.down_stride = _stack(w_down, "w_down", dtype, x.device, (E, H, I))
+    a.w_gate, a.w_up, a.w_down = w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr()
+    if dtype == torch.bfloat16:
+        if not (gate_scale is None and up_scale is None and down_scale is None):
+            raise ValueError("scales belong to float8_e4m3fn and int8 weights")
+    else:
+        if gate_scale is None or up_scale is None or down_scale is None:
+            raise ValueError(f"{dtype} weights need a scale each")
+        blocks = dtype == torch.float8_e4m3fn and gate_scale.dim() == 3
+        hb, ib = -(-H // 128), -(-I // 128)
+        a.type = (SKINNY_WEIGHTS_INT8_ROW if dtype == torch.int8 else
+                  SKINNY_WEIGHTS_E4M3_BLOCK if blocks else SKINNY_WEIGHTS_E4M3_ROW)
+        shape = (E, ib, hb) if blocks else (E, I)
+        a.up_scale_stride = _stack(gate_scale, "gate_scale", torch.float32, x.device, shape)
+        if _stack(up_scale, "up_scale", torch.float32, x.device, shape) != a.up_scale_stride:
+            raise ValueError("gate_scale and up_scale must have the same strides")
+        a.down_scale_stride = _stack(down_scale, "down_scale", torch.float32, x.device,
+                                     (E, hb, ib) if blocks else (E, H))
+        a.gate_scale, a.up_scale, a.down_scale = gate_scale.data_ptr(), up_scale.data_ptr(), down_scale.data_ptr()
+    if residual is not None:
+        a.ldr = _matrix(residual, "residual", torch.bfloat16, x.device, (M, H))
+        a.residual = residual.data_ptr()
+    if out is None:
+        out = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+    a.ldy = _matrix(out, "out", torch.bfloat16, x.device, (M, H))
+    a.y = out.data_ptr()
+    if M == 0:
+        return out
+    if workspace is None:
+        workspace = experts_workspace(M, k, E, I, x.device)
+    elif workspace.device != x.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {x.device}")
+    a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    s = _stream_handle(x.device)
+    with _on_device(x.device):
+        skinny_experts(a, s)
+    return out
+
+
 __all__ = [
     "SkinnyError", "Plan", "lib", "variants", "gemm", "gemm_pair", "gemm_pair_strided",
     "split_k_variants", "split_k_workspace", "gemm_split_k", "gemm_split_k_noalloc",
@@ -792,7 +972,10 @@ __all__ = [
     "SKINNY_ERR_LAUNCH", "SKINNY_KIND_FIXED_K", "SKINNY_KIND_LOOP_K", "SKINNY_KIND_SCALAR",
     "SKINNY_KIND_MFMA", "NormArgs", "LinearArgs", "LinearPlan", "ACTS", "rms_norm", "linear",
     "skinny_rms_norm_bf16", "skinny_rms_norm_fp8", "skinny_linear_bf16", "skinny_linear_fp8",
-    "skinny_linear_default_plan", "quantize_int8", "skinny_rms_norm_int8", "skinny_quantize_int8",
+    "skinny_linear_default_plan", "RouteArgs", "ExpertsArgs", "SCORES", "route", "experts",
+    "experts_workspace", "skinny_route", "skinny_experts", "skinny_experts_workspace_bytes",
+    "SKINNY_SCORE_SOFTMAX", "SKINNY_SCORE_SIGMOID", "SKINNY_WEIGHTS_BF16", "SKINNY_WEIGHTS_E4M3_ROW",
+    "SKINNY_WEIGHTS_E4M3_BLOCK", "SKINNY_WEIGHTS_INT8_ROW", "quantize_int8", "skinny_rms_norm_int8", "skinny_quantize_int8",
     "skinny_linear_int8", "skinny_linear_int8_default_plan", "SKINNY_LINEAR_ELEMENTS", "SKINNY_LINEAR_STREAM", "SKINNY_LINEAR_TILE",
     "SKINNY_ACT_NONE", "SKINNY_ACT_RELU", "SKINNY_ACT_GELU", "SKINNY_ACT_GELU_TANH",
     "SKINNY_ACT_SILU", "SKINNY_SCALES_ROW", "SKINNY_SCALES_BLOCK",

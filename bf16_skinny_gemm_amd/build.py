@@ -28,6 +28,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 ARCH = "gfx950"
 SOURCES = ("skinny_gemm.hip", "variants_fixed_small.hip", "variants_fixed_k4096.hip",
            "variants_fixed_k8192.hip", "variants_other.hip", "split_k.hip", "norm.hip", "linear.hip",
+           "route.hip", "experts.hip",
            "linear_stream_bf16.hip", "linear_stream_row.hip", "linear_stream_block.hip",
            "linear_stream_int8.hip", "linear_tile_bf16.hip", "linear_tile_row.hip", "linear_tile_block.hip",
            "linear_tile_int8.hip")

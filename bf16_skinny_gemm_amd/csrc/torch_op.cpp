@@ -11,8 +11,8 @@
 // (bf16_skinny_gemm_amd/torch_op.py), which this library names as the op's
 // Python module.
 //
-// The operators of include/skinny_ops.h (norms, projections with an epilogue) are
-// registered below in the same way.
+// The operators of include/skinny_ops.h (norms, projections with an epilogue) and
+// include/skinny_moe.h (router, experts) are registered below in the same way.
 #include <ATen/core/Tensor.h>
 #include <ATen/hip/EmptyTensor.h>
 #include <ATen/ops/empty.h>
@@ -24,6 +24,7 @@
 #include <climits>
 
 #include "skinny_gemm.h"
+#include "skinny_moe.h"
 #include "skinny_ops.h"
 
 namespace {
@@ -402,6 +403,149 @@ at::Tensor linear_gated_int8_gpu(const at::Tensor &x, const at::Tensor &x_scale,
     return linear_any("skinny::linear_gated_int8", at::kChar, x, &x_scale, s, 2, std::nullopt, act, out_f32);
 }
 
+// ---- operators of skinny_moe.h ---------------------------------------------------
+
+std::tuple<at::Tensor, at::Tensor> route_gpu(const at::Tensor &logits, int64_t k, c10::string_view score, const Opt &bias,
+                                             int64_t groups, int64_t kept, bool renormalize, double scale)
+{
+    const char *op = "skinny::route";
+    TORCH_CHECK_VALUE(logits.scalar_type() == at::kFloat && logits.dim() >= 1, op,
+                      ": logits must be float32 with at least one dimension, got ", logits.scalar_type(), " ", logits.sizes());
+    const int64_t E = logits.size(-1);
+    TORCH_CHECK_VALUE(E >= 1 && E <= 1024, op, ": the number of experts must be 1..1024, got ", E);
+    TORCH_CHECK_VALUE(score == "softmax" || score == "sigmoid", op, ": score must be softmax or sigmoid, got ", score);
+    TORCH_CHECK_VALUE(groups >= 1 && groups <= 64 && E % groups == 0 && kept >= 1 && kept <= groups, op,
+                      ": groups must be 1..64 and divide ", E, ", and kept 1..groups, got ", groups, " and ", kept);
+    TORCH_CHECK_VALUE(k >= 1 && k <= 64 && k <= kept * (E / groups), op, ": k must be 1..64 and at most ",
+                      kept * (E / groups), ", got ", k);
+    if (bias) {
+        check_gpu(op, logits, *bias, "bias", at::kFloat);
+        TORCH_CHECK_VALUE(bias->dim() == 1 && bias->size(0) == E && bias->is_contiguous(), op,
+                          ": bias must be a contiguous [", E, "], got ", bias->sizes());
+    }
+    const OnDevice on(logits);
+    const Rows r = rows_of(logits, E);
+    const auto shape = with_last(logits, k);
+    at::Tensor ids = output(shape, at::kInt, logits), weights = output(shape, at::kFloat, logits);
+    skinny_route_t a{};
+    a.logits = static_cast<const float *>(r.p);
+    a.ldl = r.ld;
+    a.bias = bias ? bias->data_ptr<float>() : nullptr;
+    a.ids = ids.data_ptr<int32_t>();
+    a.weights = weights.data_ptr<float>();
+    a.M = size32(op, r.M, "the number of rows");
+    a.E = (int32_t)E;
+    a.k = (int32_t)k;
+    a.score = score == "softmax" ? SKINNY_SCORE_SOFTMAX : SKINNY_SCORE_SIGMOID;
+    a.groups = (int32_t)groups;
+    a.kept = (int32_t)kept;
+    a.renormalize = renormalize;
+    a.scale = (float)scale;
+    check_status(op, skinny_route(&a, c10::hip::getCurrentHIPStream(logits.device().index()).stream()));
+    return {ids, weights};
+}
+
+// A stack of contiguous matrices or vectors, one per expert, any distance apart: the
+// distance.
+int64_t check_stack(const char *op, const at::Tensor &x, const at::Tensor &t, const char *name, at::ScalarType type,
+                    at::IntArrayRef shape)
+{
+    check_gpu(op, x, t, name, type);
+    bool inner = t.sizes() == shape;
+    int64_t size = 1;
+    for (int64_t d = t.dim() - 1; inner && d > 0; --d) {
+        inner = t.size(d) == 1 || t.stride(d) == size;
+        size *= t.size(d);
+    }
+    TORCH_CHECK_VALUE(inner, op, ": ", name, " must be ", shape, " with contiguous parts, got ", t.sizes(), " of strides ",
+                      t.strides());
+    return shape[0] > 1 ? t.stride(0) : size;
+}
+
+at::Tensor experts_gpu(const at::Tensor &x, const at::Tensor &ids, const at::Tensor &weights, const at::Tensor &w_gate,
+                       const at::Tensor &w_up, const at::Tensor &w_down, const Opt &gate_scale, const Opt &up_scale,
+                       const Opt &down_scale, const Opt &residual, c10::string_view act)
+{
+    const char *op = "skinny::experts";
+    check_matrix(op, x, at::kBFloat16);
+    const at::ScalarType type = w_gate.scalar_type();
+    TORCH_CHECK_VALUE(type == at::kBFloat16 || type == at::kChar || type == at::kFloat8_e4m3fn, op,
+                      ": w_gate must be bfloat16, int8 or float8_e4m3fn, got ", type);
+    TORCH_CHECK_VALUE(w_gate.dim() == 3, op, ": w_gate must be [E, I, H], got ", w_gate.sizes());
+    const int64_t H = x.size(-1), E = w_gate.size(0), I = w_gate.size(1);
+    check_gpu(op, x, ids, "ids", at::kInt);
+    check_gpu(op, x, weights, "weights", at::kFloat);
+    TORCH_CHECK_VALUE(ids.dim() == x.dim() && ids.sizes() == weights.sizes() &&
+                          ids.sizes().slice(0, ids.dim() - 1) == x.sizes().slice(0, x.dim() - 1),
+                      op, ": ids and weights must be [..., k] beside x ", x.sizes(), ", got ", ids.sizes(), " and ",
+                      weights.sizes());
+    const int64_t k = ids.size(-1);
+    TORCH_CHECK_VALUE(E >= 1 && E <= 1024 && k >= 1 && k <= 32 && H >= 1 && I >= 1, op,
+                      ": E must be 1..1024, k 1..32, H and I above 0, got ", E, ", ", k, ", ", H, " and ", I);
+    skinny_experts_t a{};
+    a.up_stride = check_stack(op, x, w_gate, "w_gate", type, {E, I, H});
+    TORCH_CHECK_VALUE(check_stack(op, x, w_up, "w_up", type, {E, I, H}) == a.up_stride, op,
+                      ": w_gate and w_up must have the same strides");
+    a.down_stride = check_stack(op, x, w_down, "w_down", type, {E, H, I});
+    const bool scaled = type != at::kBFloat16;
+    TORCH_CHECK_VALUE(gate_scale.has_value() == scaled && up_scale.has_value() == scaled && down_scale.has_value() == scaled,
+                      op, ": float8_e4m3fn and int8 weights need a scale each, bfloat16 ones take none");
+    a.type = SKINNY_WEIGHTS_BF16;
+    if (scaled) {
+        const bool blocks = type == at::kFloat8_e4m3fn && gate_scale->dim() == 3;
+        const int64_t hb = (H + 127) / 128, ib = (I + 127) / 128;
+        a.type = type == at::kChar ? SKINNY_WEIGHTS_INT8_ROW
+                 : blocks          ? SKINNY_WEIGHTS_E4M3_BLOCK
+                                   : SKINNY_WEIGHTS_E4M3_ROW;
+        const c10::SmallVector<int64_t, 3> up = blocks ? c10::SmallVector<int64_t, 3>{E, ib, hb} : c10::SmallVector<int64_t, 3>{E, I};
+        const c10::SmallVector<int64_t, 3> down =
+            blocks ? c10::SmallVector<int64_t, 3>{E, hb, ib} : c10::SmallVector<int64_t, 3>{E, H};
+        a.up_scale_stride = check_stack(op, x, *gate_scale, "gate_scale", at::kFloat, up);
+        TORCH_CHECK_VALUE(check_stack(op, x, *up_scale, "up_scale", at::kFloat, up) == a.up_scale_stride, op,
+                          ": gate_scale and up_scale must have the same strides");
+        a.down_scale_stride = check_stack(op, x, *down_scale, "down_scale", at::kFloat, down);
+        a.gate_scale = gate_scale->data_ptr<float>();
+        a.up_scale = up_scale->data_ptr<float>();
+        a.down_scale = down_scale->data_ptr<float>();
+    }
+    const OnDevice on(x);
+    const Rows xr = rows_of(x, H);
+    Rows rr{};
+    a.x = xr.p;
+    a.ldx = xr.ld;
+    const at::Tensor ids_c = ids.contiguous(), weights_c = weights.contiguous();
+    a.ids = ids_c.data_ptr<int32_t>();
+    a.weights = weights_c.data_ptr<float>();
+    a.w_gate = w_gate.data_ptr();
+    a.w_up = w_up.data_ptr();
+    a.w_down = w_down.data_ptr();
+    a.M = size32(op, xr.M, "the number of rows");
+    a.E = (int32_t)E;
+    a.k = (int32_t)k;
+    a.H = size32(op, H, "H");
+    a.I = size32(op, I, "I");
+    a.act = act_of(op, act);
+    if (residual) {
+        check_gpu(op, x, *residual, "residual", at::kBFloat16);
+        TORCH_CHECK_VALUE(residual->sizes() == x.sizes(), op, ": residual must have x's shape ", x.sizes(), ", got ",
+                          residual->sizes());
+        rr = rows_of(*residual, H);
+        a.residual = rr.p;
+        a.ldr = rr.ld;
+    }
+    at::Tensor y = output(x.sizes(), at::kBFloat16, x);
+    if (a.M == 0)
+        return y;
+    a.y = y.data_ptr();
+    a.ldy = H;
+    a.workspace_bytes = skinny_experts_workspace_bytes(a.M, a.k, a.E, a.I);
+    // freed when the call returns, for later work on this stream only
+    const at::Tensor workspace = output({(int64_t)a.workspace_bytes}, at::kByte, x);
+    a.workspace = workspace.data_ptr();
+    check_status(op, skinny_experts(&a, c10::hip::getCurrentHIPStream(x.device().index()).stream()));
+    return y;
+}
+
 // CPU tensors: every operator refuses them by name.
 void refuse_cpu(const c10::OperatorHandle &op, torch::jit::Stack *)
 {
@@ -434,6 +578,11 @@ TORCH_LIBRARY(skinny, m)
           "Tensor? residual=None, str act='none', bool out_f32=False) -> Tensor");
     m.def("linear_gated_int8(Tensor x, Tensor x_scale, Tensor w_gate, Tensor gate_scale, Tensor w_up, "
           "Tensor up_scale, Tensor? b_gate=None, Tensor? b_up=None, str act='silu', bool out_f32=False) -> Tensor");
+    m.def("route(Tensor logits, int k, str score='softmax', Tensor? bias=None, int groups=1, int kept=1, "
+          "bool renormalize=True, float scale=1.0) -> (Tensor, Tensor)");
+    m.def("experts(Tensor x, Tensor ids, Tensor weights, Tensor w_gate, Tensor w_up, Tensor w_down, "
+          "Tensor? gate_scale=None, Tensor? up_scale=None, Tensor? down_scale=None, Tensor? residual=None, "
+          "str act='silu') -> Tensor");
 }
 
 TORCH_LIBRARY_IMPL(skinny, CUDA, m)
@@ -452,6 +601,8 @@ TORCH_LIBRARY_IMPL(skinny, CUDA, m)
     m.impl("add_rms_norm_int8", &add_rms_norm_int8_gpu);
     m.impl("linear_int8", &linear_int8_gpu);
     m.impl("linear_gated_int8", &linear_gated_int8_gpu);
+    m.impl("route", &route_gpu);
+    m.impl("experts", &experts_gpu);
 }
 
 TORCH_LIBRARY_IMPL(skinny, CPU, m)
@@ -459,6 +610,6 @@ TORCH_LIBRARY_IMPL(skinny, CPU, m)
     m.impl("linear", &linear_cpu);
     for (const char *op : {"rms_norm", "add_rms_norm", "rms_norm_fp8", "add_rms_norm_fp8", "linear_act",
                            "linear_gated", "linear_fp8", "linear_gated_fp8", "quantize_int8", "rms_norm_int8",
-                           "add_rms_norm_int8", "linear_int8", "linear_gated_int8"})
+                           "add_rms_norm_int8", "linear_int8", "linear_gated_int8", "route", "experts"})
         m.impl(op, torch::CppFunction::makeFromBoxedFunction<&refuse_cpu>());
 }

@@ -19,8 +19,8 @@ linear path otherwise. Here:
   module hook), else they raise;
 * :func:`install` swaps the forward of ``nn.Linear`` modules for the routed one;
 * ``rms_norm``, ``add_rms_norm``, ``linear_act`` and ``linear_gated``, their 8-bit forms with
-  ``_fp8`` and ``_int8`` behind the name, and ``quantize_int8`` (``torch.ops.skinny.*``, same
-  registration) are the operators around the projection, for any number of rows;
+  ``_fp8`` and ``_int8`` behind the name, ``quantize_int8``, ``route`` and ``experts``
+  (``torch.ops.skinny.*``, same registration) are the operators around the projection, for any number of rows;
   :func:`install` with ``fused=True`` routes biased ``nn.Linear`` layers and
   ``nn.RMSNorm`` modules to them.
 
@@ -42,9 +42,11 @@ from torch.autograd import forward_ad
 from torch.overrides import TorchFunctionMode
 
 from . import _on_device, _stream_handle, lib, skinny_gemm_bf16
+from . import experts as _experts_call
 from . import linear as _linear_call
 from . import quantize_int8 as _quantize_call
 from . import rms_norm as _norm_call
+from . import route as _route_call
 from .build import TORCH_OP_PATH
 
 _ARCH_OK: dict[int, bool] = {}
@@ -154,6 +156,11 @@ _SCHEMAS = (
     "linear_gated_int8(Tensor x, Tensor x_scale, Tensor w_gate, Tensor gate_scale, Tensor w_up, "
     "Tensor up_scale, Tensor? b_gate=None, Tensor? b_up=None, str act='silu', "
     "bool out_f32=False) -> Tensor",
+    "route(Tensor logits, int k, str score='softmax', Tensor? bias=None, int groups=1, int kept=1, "
+    "bool renormalize=True, float scale=1.0) -> (Tensor, Tensor)",
+    "experts(Tensor x, Tensor ids, Tensor weights, Tensor w_gate, Tensor w_up, Tensor w_down, "
+    "Tensor? gate_scale=None, Tensor? up_scale=None, Tensor? down_scale=None, Tensor? residual=None, "
+    "str act='silu') -> Tensor",
 )
 
 
@@ -196,6 +203,23 @@ def _linear_py(x, weight, bias, residual, act, out_f32, W_up=None, bias_up=None,
     return y.reshape(*x.shape[:-1], N)
 
 
+def _route_py(logits, k, score="softmax", bias=None, groups=1, kept=1, renormalize=True, scale=1.0):
+    got = _route_call(logits.reshape(-1, logits.shape[-1]), k, score, bias, groups, kept, renormalize, scale)
+    return tuple(t.reshape(*logits.shape[:-1], k) for t in got)
+
+
+def _experts_py(x, ids, weights, w_gate, w_up, w_down, gate_scale=None, up_scale=None, down_scale=None,
+                residual=None, act="silu"):
+    H, k = x.shape[-1], ids.shape[-1]
+    if ids.shape != (*x.shape[:-1], k) or ids.shape != weights.shape:
+        raise ValueError(f"ids and weights must be [..., k] beside x {list(x.shape)}, got {list(ids.shape)} and "
+                         f"{list(weights.shape)}")
+    M = math.prod(x.shape[:-1])
+    return _experts_call(x.reshape(M, H), ids.reshape(M, k).contiguous(), weights.reshape(M, k).contiguous(), w_gate, w_up,
+                         w_down, gate_scale, up_scale, down_scale,
+                         None if residual is None else residual.reshape(M, H), act).reshape(x.shape)
+
+
 _PY_KERNELS = {
     "rms_norm": lambda x, w, eps: _norm_py(x, w, eps),
     "add_rms_norm": lambda x, r, w, eps: _norm_py(x, w, eps, r),
@@ -215,6 +239,8 @@ _PY_KERNELS = {
         _int8(x), w, b, r, act, f32, x_scale=xs, w_scale=ws),
     "linear_gated_int8": lambda x, xs, w, ws, u, us, b=None, bu=None, act="silu", f32=False: _linear_py(
         _int8(x), w, b, None, act, f32, u, bu, xs, ws, us),
+    "route": _route_py,
+    "experts": _experts_py,
 }
 
 
@@ -264,6 +290,10 @@ _FAKES = {
     out_f32=False: _y_fake(x, weight.shape[0], out_f32),
     "linear_gated_int8": lambda x, x_scale, w_gate, gate_scale, w_up, up_scale, b_gate=None, b_up=None,
     act="silu", out_f32=False: _y_fake(x, w_gate.shape[0], out_f32),
+    "route": lambda logits, k, score="softmax", bias=None, groups=1, kept=1, renormalize=True, scale=1.0: (
+        logits.new_empty((*logits.shape[:-1], k), dtype=torch.int32), logits.new_empty((*logits.shape[:-1], k))),
+    "experts": lambda x, ids, weights, w_gate, w_up, w_down, gate_scale=None, up_scale=None, down_scale=None,
+    residual=None, act="silu": x.new_empty(x.shape),
 }
 
 for _schema in _SCHEMAS:
@@ -286,6 +316,8 @@ rms_norm_int8 = torch.ops.skinny.rms_norm_int8.default
 add_rms_norm_int8 = torch.ops.skinny.add_rms_norm_int8.default
 linear_int8 = torch.ops.skinny.linear_int8.default
 linear_gated_int8 = torch.ops.skinny.linear_gated_int8.default
+route = torch.ops.skinny.route.default
+experts = torch.ops.skinny.experts.default
 
 
 _func_level = torch._C._functorch.maybe_current_level
@@ -426,4 +458,4 @@ def install(module: torch.nn.Module, fallback: bool = True, fused: bool = False)
 __all__ = ["linear", "skinny_linear", "install", "qualifies", "qualifies_fused", "CPP_OP", "FUSED_ROWS",
            "rms_norm", "add_rms_norm", "rms_norm_fp8", "add_rms_norm_fp8", "linear_act", "linear_gated",
            "linear_fp8", "linear_gated_fp8", "quantize_int8", "rms_norm_int8", "add_rms_norm_int8",
-           "linear_int8", "linear_gated_int8"]
+           "linear_int8", "linear_gated_int8", "route", "experts"]
