@@ -120,66 +120,29 @@ __device__ __forceinline__ void read_x(const uint8_t *row, int g, int swizzle, i
     }
 }
 
+// Bytes of a stage: weights, x or h, and what belongs to them.
+template <int TYPE, int BM>
+constexpr int up_stage() { return 2048 + planes<TYPE>() * BM * 128 + (TYPE == kWBf16 ? 0 : 64); }
+template <int TYPE, int NB, int BM>
+constexpr int down_stage() { return NB * 128 + planes<TYPE>() * BM * 128 + BM * 16 + (TYPE == kWBf16 ? 0 : 64); }
+
 // ---- the pairs by expert -----------------------------------------------------------
 
-struct Tile {
-    int expert, first, pairs;  // expert < 0: there is no such tile
+// The plan of a pass in LDS, made by every block for itself: the tiles (expert | pairs << 10 |
+// first pair << 16) and each sorted pair's token.
+struct Plan {
+    unsigned tiles[kMostTiles];
+    uint8_t tokens[kMostPairs];
+    int count;
 };
 
-// Pairs of up to one wave: every wave sorts them in its lanes. Returns tile t; *pair: in lane
-// r the r-th pair of the tile.
-template <int BM>
-__device__ __forceinline__ Tile find_tile_wave(const ExpertArgs &a, int P, int t, int *pair)
-{
-    const int lane = threadIdx.x & 63;
-    int id = lane < P ? a.ids[lane] : -1;
-    id = (unsigned)id < (unsigned)a.E ? id : 0x7FFFFFFF;
-    int rank = 0, less = 0;
-    for (int q = 0; q < P; ++q) {
-        const int o = __builtin_amdgcn_readlane(id, q);
-        rank += o == id && q < lane;
-        less += o < id;
-    }
-    const int pos = lane < P ? less + rank : lane;  // where the pair goes
-    const int sid = __builtin_amdgcn_ds_permute(pos * 4, id);
-    const int srank = __builtin_amdgcn_ds_permute(pos * 4, rank);
-    const int spair = __builtin_amdgcn_ds_permute(pos * 4, lane);
-    const unsigned long long firsts = __ballot(lane < P && sid != 0x7FFFFFFF && srank % BM == 0);
-    const int before = __builtin_amdgcn_mbcnt_hi((unsigned)(firsts >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)firsts, 0));
-    const unsigned long long at = __ballot((firsts >> lane & 1) && before == t);
-    if (!at)
-        return Tile{-1, 0, 0};
-    const int first = __builtin_ctzll(at);
-    const int expert = __builtin_amdgcn_readlane(sid, first);
-    const int pairs = __popcll(__ballot(sid == expert && lane >= first && lane < first + BM));
-    *pair = __builtin_amdgcn_ds_bpermute((first + lane) * 4, spair);
-    return Tile{expert, first, pairs};
-}
-
-// More pairs: counted by expert in LDS by the whole block.
-struct Counts {
-    int pairs[skg_host::kMaxExperts];   // of each expert; then, of the plan, its first pair
-    uint16_t ids[kMostPairs];           // of each pair; 0xFFFF: none
-    int found[4];
-    uint16_t list[64];                  // pairs of the tile
+// What making it takes beside: which tokens name an expert, and where its pairs start.
+struct Scratch {
+    unsigned named[skg_host::kMaxExperts][skg_host::kExpertsRows / 32];
+    int first[skg_host::kMaxExperts], tile[skg_host::kMaxExperts];
+    uint16_t ids[kMostPairs];  // 0xFFFF: none
+    int twice;                 // some token names an expert twice
 };
-
-// Ends behind a barrier.
-template <int THREADS>
-__device__ __forceinline__ void count_pairs(const ExpertArgs &a, int P, Counts &c)
-{
-    for (int e = threadIdx.x; e < a.E; e += THREADS)
-        c.pairs[e] = 0;
-    __syncthreads();
-    for (int p = threadIdx.x; p < P; p += THREADS) {
-        const int id = a.ids[p];
-        const bool in = (unsigned)id < (unsigned)a.E;
-        c.ids[p] = in ? (uint16_t)id : (uint16_t)0xFFFF;
-        if (in)
-            atomicAdd(&c.pairs[id], 1);  // integers: the order changes nothing
-    }
-    __syncthreads();
-}
 
 // Inclusive sums over the lanes of a wave.
 __device__ __forceinline__ int wave_scan(int v)
@@ -193,265 +156,356 @@ __device__ __forceinline__ int wave_scan(int v)
     return v;
 }
 
-// The first wave: this lane's experts [lo, hi), and the pairs and tiles before them.
-template <int BM>
-__device__ __forceinline__ void before_lane(const ExpertArgs &a, const Counts &c, int &lo, int &hi, int &pairs, int &tiles)
+__device__ __forceinline__ void put_entry(const ExpertArgs &a, int at, int p)
 {
-    const int lane = threadIdx.x & 63, per = (a.E + 63) / 64;
-    lo = lane * per < a.E ? lane * per : a.E;
-    hi = lo + per < a.E ? lo + per : a.E;
-    int np = 0, nt = 0;
-    for (int e = lo; e < hi; ++e) {
-        np += c.pairs[e];
-        nt += (c.pairs[e] + BM - 1) / BM;
-    }
-    pairs = wave_scan(np) - np;
-    tiles = wave_scan(nt) - nt;
+    a.entries[at] = u32x4{(unsigned)(p / a.k), __builtin_bit_cast(unsigned, a.weights[p]), 0, 0};
 }
 
-// Tile t of the block's counted pairs, its pairs in c.list.
+// Up to 64 pairs: the first wave sorts them in its lanes, by expert and then by pair.
 template <int BM>
-__device__ __forceinline__ Tile find_tile_block(const ExpertArgs &a, int P, int t, Counts &c)
+__device__ __forceinline__ void plan_wave(const ExpertArgs &a, int P, Plan &plan)
 {
-    if (threadIdx.x < 64) {
-        const int lane = threadIdx.x;
-        if (lane == 0)
-            c.found[0] = -1;
-        int lo, hi, pairs, tiles;
-        before_lane<BM>(a, c, lo, hi, pairs, tiles);
-        for (int e = lo; e < hi; ++e) {
-            const int n = c.pairs[e], nt = (n + BM - 1) / BM;
-            if (t >= tiles && t < tiles + nt) {
-                const int r = (t - tiles) * BM;
-                c.found[0] = e;
-                c.found[1] = pairs + r;
-                c.found[2] = n - r < BM ? n - r : BM;
-                c.found[3] = r;
-            }
-            pairs += n;
-            tiles += nt;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-        const int e = c.found[0], r0 = c.found[3], n = c.found[2];
-        if (e >= 0)
-            for (int p0 = 0, seen = 0; p0 < P && seen < r0 + n; p0 += 64) {
-                const bool mine = p0 + lane < P && c.ids[p0 + lane] == e;
-                const unsigned long long b = __ballot(mine);
-                const int r = seen + __builtin_amdgcn_mbcnt_hi((unsigned)(b >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)b, 0)) - r0;
-                if (mine && r >= 0 && r < n)
-                    c.list[r] = (uint16_t)(p0 + lane);
-                seen += __popcll(b);
-            }
+    if (threadIdx.x >= 64)
+        return;
+    const int lane = threadIdx.x;
+    const int named = lane < P ? a.ids[lane] : -1;
+    const bool in = (unsigned)named < (unsigned)a.E;
+    const int id = in ? named : 0x7FFFFFFF;
+    int rank = 0, less = 0, pairs = 0;
+    for (int q = 0; q < P; ++q) {
+        const int o = __builtin_amdgcn_readlane(id, q);
+        rank += o == id && q < lane;
+        pairs += o == id;
+        less += o < id;
     }
-    __syncthreads();
-    return Tile{__builtin_amdgcn_readfirstlane(c.found[0]), __builtin_amdgcn_readfirstlane(c.found[1]),
-                __builtin_amdgcn_readfirstlane(c.found[2])};
+    const int pos = less + rank;
+    const bool first = in && rank % BM == 0;
+    // the tiles before this one: the first pairs of tiles at smaller places
+    int before = 0;
+    for (int q = 0; q < P; ++q) {
+        const int o = __builtin_amdgcn_readlane(first ? pos : 0x7FFFFFFF, q);
+        before += o < pos;
+    }
+    if (in) {
+        plan.tokens[pos] = (uint8_t)(lane / a.k);
+        if (blockIdx.x == 0)
+            put_entry(a, pos, lane);
+    }
+    if (first)
+        plan.tiles[before] = (unsigned)id | (unsigned)(pairs - rank < BM ? pairs - rank : BM) << 10 | (unsigned)pos << 16;
+    const int count = __popcll(__ballot(first));
+    if (lane == 0)
+        plan.count = count;
 }
 
-// The tiles and the sorted pairs for the second kernel, written by one block of the first.
+// More: a bit for each token in a mask of each expert, so that a pair's place is the number of
+// bits before its own. Only where a token names an expert twice are pairs counted one by one.
 template <int BM, int THREADS>
-__device__ __forceinline__ void write_plan(const ExpertArgs &a, int P, Counts &c)
+__device__ __forceinline__ void plan_block(const ExpertArgs &a, int P, Plan &plan, Scratch &s)
 {
-    if (threadIdx.x < 64) {
-        int lo, hi, pairs, tiles;
-        before_lane<BM>(a, c, lo, hi, pairs, tiles);
-        for (int e = lo; e < hi; ++e) {
-            const int n = c.pairs[e];
-            for (int r = 0; r < n; r += BM)
-                a.plan[4 + tiles++] = (unsigned)e | (unsigned)(n - r < BM ? n - r : BM) << 10 | (unsigned)(pairs + r) << 16;
-            c.pairs[e] = pairs;
-            pairs += n;
-        }
-        if (threadIdx.x == 63)
-            a.plan[0] = (unsigned)tiles;
+    const int t = threadIdx.x;
+    constexpr int WORDS = skg_host::kExpertsRows / 32;
+    for (int i = t; i < a.E * WORDS; i += THREADS)
+        s.named[0][i] = 0;
+    if (t == 0)
+        s.twice = 0;
+    __syncthreads();
+    for (int p = t; p < P; p += THREADS) {
+        const int id = a.ids[p], m = p / a.k;
+        const bool in = (unsigned)id < (unsigned)a.E;
+        s.ids[p] = in ? (uint16_t)id : (uint16_t)0xFFFF;
+        if (in && (atomicOr(&s.named[id][m / 32], 1u << (m % 32)) >> (m % 32) & 1))
+            s.twice = 1;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += THREADS) {
-        int at = c.pairs[e];
-        for (int p = 0; p < P; ++p)
-            if (c.ids[p] == e)
-                a.entries[at++] = u32x4{(unsigned)(p / a.k), __builtin_bit_cast(unsigned, a.weights[p]), 0, 0};
+    const bool twice = s.twice != 0;
+    auto pairs_of = [&](int e) {
+        int n = 0;
+        if (!twice) {
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w)
+                n += __popc(s.named[e][w]);
+        } else {
+            for (int p = 0; p < P; ++p)
+                n += s.ids[p] == e;
+        }
+        return n;
+    };
+    for (int e = t; e < a.E; e += THREADS)
+        s.first[e] = pairs_of(e);
+    __syncthreads();
+    if (t < 64) {
+        const int per = (a.E + 63) / 64, lo = t * per < a.E ? t * per : a.E, hi = lo + per < a.E ? lo + per : a.E;
+        int np = 0, nt = 0;
+        for (int e = lo; e < hi; ++e) {
+            np += s.first[e];
+            nt += (s.first[e] + BM - 1) / BM;
+        }
+        int pairs = wave_scan(np) - np, tiles = wave_scan(nt) - nt;
+        if (t == 63)
+            plan.count = tiles + nt;
+        for (int e = lo; e < hi; ++e) {
+            const int n = s.first[e];
+            s.first[e] = pairs;
+            s.tile[e] = tiles;
+            pairs += n;
+            tiles += (n + BM - 1) / BM;
+        }
+    }
+    __syncthreads();
+    for (int e = t; e < a.E; e += THREADS) {
+        const int n = pairs_of(e), first = s.first[e], tile = s.tile[e];
+        for (int r = 0; r < n; r += BM)
+            plan.tiles[tile + r / BM] = (unsigned)e | (unsigned)(n - r < BM ? n - r : BM) << 10 | (unsigned)(first + r) << 16;
+    }
+    for (int p = t; p < P; p += THREADS) {
+        const int e = s.ids[p], m = p / a.k;
+        if (e == 0xFFFF)
+            continue;
+        int at = s.first[e];
+        if (!twice) {
+            for (int w = 0; w < m / 32; ++w)
+                at += __popc(s.named[e][w]);
+            at += __popc(s.named[e][m / 32] & ((1u << (m % 32)) - 1));
+        } else {
+            for (int q = 0; q < p; ++q)
+                at += s.ids[q] == e;
+        }
+        plan.tokens[at] = (uint8_t)m;
+        if (blockIdx.x == 0)
+            put_entry(a, at, p);
     }
 }
 
 // ---- up ------------------------------------------------------------------------------
 
-// blockIdx.x == 0 writes the plan; the others take a tile each (blockIdx.x - 1) / nt and NB
-// features. WAVE: the pairs fit one wave.
-template <int TYPE, int NB, int BM, int RING, int WAVES, bool WAVE>
-__global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a, int nt)
+// A unit is 8 features of both weights (16 rows of an instruction: gate, then up) for one
+// tile. Each block takes a run of units and each of its waves an equal run of their stages,
+// its loads going on from one unit to the next; only a unit that lies in several waves' runs
+// waits for the block's end, where its parts are added in the order of the waves. The
+// instruction's halves meet by an exchange of lanes, so a unit needs no barrier.
+// WAVE: the pairs fit one wave.
+template <int TYPE, int BM, int RING, int WAVES, bool WAVE>
+__global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
 {
     constexpr bool BLOCK = TYPE == kWBlock;
     constexpr int PLANES = planes<TYPE>();
-    constexpr bool HALF = NB == 8;
-    constexpr int BN = 2 * NB, TN = BN / 16, TM = (BM + 15) / 16;
-    constexpr int TF = HALF ? 1 : NB / 16;
-    constexpr int XAT = BN * 128, XPLANE = BM * 128, SAT = XAT + PLANES * XPLANE;
-    constexpr int STAGE = SAT + (BLOCK ? 512 : 0);
-    constexpr int LOADS = BN / 8 + PLANES * BM / 8 + (BLOCK ? 2 : 0);
-    constexpr int PART = WAVES * TN * TM * 1024, RINGS = WAVES * RING * STAGE;
-    constexpr int PLAN = (int)sizeof(Counts);
-    constexpr int SMEM = RINGS > PART ? (RINGS > PLAN ? RINGS : PLAN) : (PART > PLAN ? PART : PLAN);
-    static_assert(BM % 8 == 0 && BM <= 64 && 128 % NB == 0 && (RING - 1) * LOADS < 64, "tile");
+    constexpr int TM = (BM + 15) / 16;
+    constexpr int XAT = 16 * 128, XPLANE = BM * 128, SAT = XAT + PLANES * XPLANE;
+    constexpr int STAGE = up_stage<TYPE, BM>();
+    constexpr int LOADS = 2 + PLANES * BM / 8 + (TYPE == kWBf16 ? 0 : 2);
+    constexpr int RINGS = WAVES * RING * STAGE;
+    constexpr int SMEM = !WAVE && (int)sizeof(Scratch) > RINGS ? (int)sizeof(Scratch) : RINGS;
+    static_assert(BM % 8 == 0 && BM <= 32 && (RING - 1) * LOADS < 64 && RING * STAGE >= TM * 1024, "tile");
     __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM];
-    Counts &counts = *reinterpret_cast<Counts *>(smem);
+    __shared__ Plan plan;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i16 = lane & 15, g = lane >> 4;
     const int P = a.M * a.k;
-    if (blockIdx.x == 0) {
-        count_pairs<WAVES * 64>(a, P, counts);
-        write_plan<BM, WAVES * 64>(a, P, counts);
-        return;
+    if constexpr (WAVE)
+        plan_wave<BM>(a, P, plan);
+    else
+        plan_block<BM, WAVES * 64>(a, P, plan, *reinterpret_cast<Scratch *>(smem));
+    __syncthreads();
+    const int tiles = __builtin_amdgcn_readfirstlane(plan.count);
+    if (blockIdx.x == 0) {  // for the second kernel
+        for (int i = threadIdx.x; i < tiles; i += WAVES * 64)
+            a.plan[4 + i] = plan.tiles[i];
+        if (threadIdx.x == 0)
+            a.plan[0] = (unsigned)tiles;
     }
-    const int t = (int)(blockIdx.x - 1) / nt, n0 = (int)(blockIdx.x - 1) % nt * NB;
-    Tile tile;
-    int pair = 0;
-    if constexpr (WAVE) {
-        tile = find_tile_wave<BM>(a, P, t, &pair);
-    } else {
-        count_pairs<WAVES * 64>(a, P, counts);
-        tile = find_tile_block<BM>(a, P, t, counts);
-        pair = counts.list[lane];
-        __syncthreads();  // the ring is written over the counts
-    }
-    if (tile.expert < 0)
-        return;
 
     const int KB = TYPE == kWBf16 ? a.H * 2 : a.H;
     const int stages = (KB + 127) / 128;
-    const int vn = a.I - n0 < NB ? a.I - n0 : NB;
-    const int hb = (a.H + 127) / 128;
-    u32x4 wr[2], wsr[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        wr[q] = rsrc_words(a.w[q] + tile.expert * a.up_bytes + (int64_t)n0 * KB, (unsigned)vn * (unsigned)KB);
-        if constexpr (BLOCK)
-            wsr[q] = rsrc_words(a.s[q] + tile.expert * a.up_scales + (int64_t)(n0 / 128) * hb, (unsigned)hb * 4u);
-    }
+    const int nf = (a.I + 7) / 8, hb = (a.H + 127) / 128;
+    const int64_t units = (int64_t)tiles * nf;
+    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+    const int64_t total = (u1 - u0) * stages;  // of the block
+    const int64_t from = total * wave / WAVES, to = total * (wave + 1) / WAVES;
+    const int n = (int)(to - from);  // stages of this wave
     const unsigned ldx = (unsigned)a.ldx * 2u, XB = (unsigned)a.H * 2u;
     const u32x4 xr = rsrc_words(a.x, (unsigned)(a.M - 1) * ldx + XB);
-    const uint8_t *ring = smem + wave * RING * STAGE;
+    uint8_t *ring = smem + wave * RING * STAGE;
     const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem + wave * RING * STAGE;
     const int lrow = lane >> 3;
     const unsigned piece = (unsigned)((lane & 7) ^ lrow) * 16u;
-    // the rows of x that this lane loads pieces of
-    unsigned xat[BM / 8];
-#pragma unroll
-    for (int c = 0; c < BM / 8; ++c) {
-        const int r = c * 8 + lrow, p = __builtin_amdgcn_ds_bpermute(r * 4, pair);
-        xat[c] = r < tile.pairs ? (unsigned)(p / a.k) * ldx : kOutOfRange;
-    }
 
-    auto issue = [&](int s, int slot) {
-        const unsigned k = (unsigned)s * 128u + piece;
+    // the unit and stage that are loaded next
+    const int64_t begin = u0 + from / stages;
+    int it = (int)(begin / nf), iu = (int)(begin % nf), is = (int)(from % stages);
+    u32x4 wr[2], sr[2];
+    unsigned xat[BM / 8];  // the rows of x that this lane loads pieces of
+    auto enter_tile = [&] {
+        const unsigned v = __builtin_amdgcn_readfirstlane((int)plan.tiles[it]);
+        const int pairs = (int)(v >> 10 & 63u), first = (int)(v >> 16);
+#pragma unroll
+        for (int c = 0; c < BM / 8; ++c) {
+            const int r = c * 8 + lrow;
+            xat[c] = r < pairs ? (unsigned)plan.tokens[first + r] * ldx : kOutOfRange;
+        }
+    };
+    auto enter_unit = [&] {
+        const int e = (int)(__builtin_amdgcn_readfirstlane((int)plan.tiles[it]) & 1023u);
+        const int n0 = iu * 8, vn = a.I - n0 < 8 ? a.I - n0 : 8;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            wr[q] = rsrc_words(a.w[q] + e * a.up_bytes + (int64_t)n0 * KB, (unsigned)vn * (unsigned)KB);
+            if constexpr (BLOCK)
+                sr[q] = rsrc_words(a.s[q] + e * a.up_scales + (int64_t)(n0 / 128) * hb, (unsigned)hb * 4u);
+            else if constexpr (scaled_rows(TYPE))
+                sr[q] = rsrc_words(a.s[q] + e * a.up_scales + n0, (unsigned)vn * 4u);
+        }
+    };
+    auto issue = [&](int slot) {
+        const unsigned k = (unsigned)is * 128u + piece;
         const unsigned lds = lds0 + (unsigned)(slot * STAGE);
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int c = 0; c < NB / 8; ++c)
-                load_to_lds<true>(wr[q], k < (unsigned)KB ? (unsigned)(c * 8 + lrow) * (unsigned)KB + k : kOutOfRange,
-                                  lds + (unsigned)(q * NB + c * 8) * 128u);
+        const unsigned at = k < (unsigned)KB ? (unsigned)lrow * (unsigned)KB + k : kOutOfRange;
+        load_to_lds<true>(wr[0], at, lds);
+        load_to_lds<true>(wr[1], at, lds + 1024u);
 #pragma unroll
         for (int h = 0; h < PLANES; ++h) {
-            const unsigned b = (unsigned)(s * PLANES + h) * 128u + piece;
+            const unsigned b = (unsigned)(is * PLANES + h) * 128u + piece;
 #pragma unroll
             for (int c = 0; c < BM / 8; ++c)
                 load_to_lds(xr, b < XB && xat[c] != kOutOfRange ? xat[c] + b : kOutOfRange,
                             lds + XAT + (unsigned)(h * XPLANE + c * 1024));
         }
-        if constexpr (BLOCK) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                load4_to_lds(wsr[q], (unsigned)s * 4u, lds + SAT + 256u * q);
+        if constexpr (TYPE != kWBf16) {  // 8 floats of each weight: its features' scales, or the block's
+            const unsigned f = BLOCK ? (unsigned)is * 4u : (unsigned)(lane & 7) * 4u;
+            if (lane < 8) {
+                load4_to_lds(sr[0], f, lds + SAT);
+                load4_to_lds(sr[1], f, lds + SAT + 32u);
+            }
+        }
+        if (++is == stages) {
+            is = 0;
+            if (++iu == nf) {
+                iu = 0;
+                if (++it < tiles)
+                    enter_tile();
+            }
+            if (it < tiles)
+                enter_unit();
         }
     };
 
-    f32x4 acc[TN][TM];
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
+    f32x4 acc[TM], head[TM] = {}, scale = {1.0f, 1.0f, 1.0f, 1.0f};  // head: see below
+    auto clear = [&] {
 #pragma unroll
         for (int j = 0; j < TM; ++j)
-            acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    clear();
+    // h of a whole unit: lanes 0..31 hold the gate's sums, 32..63 the up projection's
+    auto finish = [&](int t, int u) {
+        const unsigned v = __builtin_amdgcn_readfirstlane((int)plan.tiles[t]);
+        const int pairs = (int)(v >> 10 & 63u), first = (int)(v >> 16), f = u * 8 + (g & 1) * 4;
 #pragma unroll
-    for (int d = 0; d < RING; ++d)
-        if (wave + d * WAVES < stages)
-            issue(wave + d * WAVES, d);
+        for (int j = 0; j < TM; ++j) {
+            f32x4 z = acc[j], o;
+            if constexpr (scaled_rows(TYPE))
+                z *= scale;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = __shfl_xor(z[e], 32, 64);
+            const int r = j * 16 + i16;
+            if (lane < 32 && r < pairs && f < a.I) {  // I is a multiple of 8: all four are there
+                z = activate4(z, a.act) * o;
+                *reinterpret_cast<u32x2 *>(a.h + (int64_t)(first + r) * a.I + f) =
+                    u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+            }
+        }
+    };
+
+    // the unit and stage that are multiplied next, and whether its sums began in this wave
+    int ct = it, cu = iu, cs = is;
+    bool whole = cs == 0;
+    if (n > 0) {
+        enter_tile();
+        enter_unit();
+#pragma unroll
+        for (int d = 0; d < RING; ++d)
+            if (d < n)
+                issue(d);
+    }
     int slot = 0;
-    for (int s = wave; s < stages; s += WAVES) {
-        if (s + (RING - 1) * WAVES < stages)
+    for (int s = 0; s < n; ++s) {
+        if (s + RING <= n)
             stage_wait<(RING - 1) * LOADS>();
         else
             stage_wait<0>();
         const uint8_t *st = ring + slot * STAGE;
-        Fragment<TYPE> af[TN];
+        Fragment<TYPE> af;
         u32x4 bf[TM][2 * PLANES];
-        float sc[TN];
-#pragma unroll
-        for (int i = 0; i < TN; ++i)
-            af[i].read(st + (i * 16 + i16) * 128, g, i16 & 7);
+        float sc = 1.0f;
+        const bool end = ++cs == stages;
+        af.read(st + i16 * 128, g, i16 & 7);
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
             const int r = BM == 8 ? i16 & 7 : j * 16 + i16;
             read_x<TYPE>(st + XAT + r * 128, g, r & 7, XPLANE, bf[j]);
         }
-        if constexpr (BLOCK) {
-            const float *f = reinterpret_cast<const float *>(st + SAT);
-#pragma unroll
-            for (int i = 0; i < TN; ++i)
-                sc[i] = f[64 * (HALF ? g >> 1 : i / TF) + lane];
-        }
+        if constexpr (BLOCK)
+            sc = *reinterpret_cast<const float *>(st + SAT + (g >> 1) * 32);
+        else if constexpr (scaled_rows(TYPE))
+            scale = *reinterpret_cast<const f32x4 *>(st + SAT + g * 16);
         lds_read_wait();  // the stage is in registers: its slot may be written again
-        if (s + RING * WAVES < stages)
-            issue(s + RING * WAVES, slot);
+        if (s + RING < n)
+            issue(slot);
         slot = slot + 1 == RING ? 0 : slot + 1;
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
+        for (int j = 0; j < TM; ++j) {
+            f32x4 p = BLOCK ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[j];
 #pragma unroll
-            for (int j = 0; j < TM; ++j) {
-                f32x4 p = BLOCK ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j];
+            for (int q = 0; q < 2 * PLANES; ++q)
+                p = mfma_bf16(af.v[q], bf[j][q], p);
+            if constexpr (BLOCK) {
 #pragma unroll
-                for (int q = 0; q < 2 * PLANES; ++q)
-                    p = mfma_bf16(af[i].v[q], bf[j][q], p);
-                if constexpr (BLOCK) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[i][j][e] = __builtin_fmaf(p[e], sc[i], acc[i][j][e]);
-                } else {
-                    acc[i][j] = p;
-                }
+                for (int e = 0; e < 4; ++e)
+                    acc[j][e] = __builtin_fmaf(p[e], sc, acc[j][e]);
+            } else {
+                acc[j] = p;
             }
+        }
+        if (end) {
+            cs = 0;
+            if (whole) {
+                finish(ct, cu);
+            } else {  // the end of a unit that an earlier wave began: the rest of its ring is
+                      // still being loaded, so the sums wait in registers
+#pragma unroll
+                for (int j = 0; j < TM; ++j)
+                    head[j] = acc[j];
+            }
+            whole = true;
+            clear();
+            if (++cu == nf) {
+                cu = 0;
+                ++ct;
+            }
+        }
     }
-
-    // the waves' sums meet in LDS, added in the order of the waves
+    // Units in several runs: a wave whose run began inside one leaves that part of its sums, and
+    // the wave that began it adds them up.
+    const bool inside = from % stages != 0;             // the run began inside a unit
+    const bool through = inside && !whole;              // and did not reach its end
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+        if (inside)
+            *reinterpret_cast<f32x4 *>(ring + (j * 64 + lane) * 16) = through ? acc[j] : head[j];
     __syncthreads();
-    f32x4 *part = reinterpret_cast<f32x4 *>(smem);
+    if (n > 0 && whole && cs != 0) {
+        const int64_t unit_end = to - cs + stages;
+        for (int w = wave + 1; w < WAVES; ++w) {
 #pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int j = 0; j < TM; ++j)
-            part[((wave * TN + i) * TM + j) * 64 + lane] = acc[i][j];
-    __syncthreads();
-    constexpr int SLOTS = HALF ? 32 : 64;  // lanes that hold outputs of the gate
-    for (int o = threadIdx.x; o < TF * TM * SLOTS; o += WAVES * 64) {
-        const int l = o % SLOTS, j = o / SLOTS % TM, i = o / SLOTS / TM;
-        const int r = j * 16 + (l & 15), n = n0 + i * 16 + (l >> 4) * 4;
-        if (r >= tile.pairs || n >= a.I)
-            continue;
-        f32x4 z = f32x4{0.0f, 0.0f, 0.0f, 0.0f}, u = z;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            z += part[((w * TN + i) * TM + j) * 64 + l];
-            u += HALF ? part[(w * TM + j) * 64 + SLOTS + l] : part[((w * TN + TF + i) * TM + j) * 64 + l];
+            for (int j = 0; j < TM; ++j)
+                acc[j] += *reinterpret_cast<const f32x4 *>(smem + w * RING * STAGE + (j * 64 + lane) * 16);
+            if (total * (w + 1) / WAVES >= unit_end)
+                break;
         }
-        // I is a multiple of 8: all four are there
-        if constexpr (scaled_rows(TYPE)) {
-            z *= *reinterpret_cast<const f32x4_any *>(a.s[0] + tile.expert * a.up_scales + n);
-            u *= *reinterpret_cast<const f32x4_any *>(a.s[1] + tile.expert * a.up_scales + n);
-        }
-        z = activate4(z, a.act) * u;
-        *reinterpret_cast<u32x2 *>(a.h + (int64_t)(tile.first + r) * a.I + n) = u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+        finish(ct, cu);
     }
 }
 
@@ -464,8 +518,8 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
     constexpr bool BLOCK = TYPE == kWBlock;
     constexpr int PLANES = planes<TYPE>();
     constexpr int TM = (BM + 15) / 16;
-    constexpr int XAT = NB * 128, XPLANE = BM * 128, EAT = XAT + PLANES * XPLANE;
-    constexpr int STAGE = EAT + 1024 + (TYPE == kWBf16 ? 0 : 256);  // a load of entries takes 64 places
+    constexpr int XAT = NB * 128, XPLANE = BM * 128, EAT = XAT + PLANES * XPLANE, SAT = EAT + BM * 16;
+    constexpr int STAGE = down_stage<TYPE, NB, BM>();
     constexpr int LOADS = NB / 8 + PLANES * BM / 8 + 1 + (TYPE == kWBf16 ? 0 : 1);
     constexpr int OUTS = MC * NB;  // floats of a wave
     static_assert((NB == 8 || NB == 16) && BM % 8 == 0 && BM <= 32 && (RING - 1) * LOADS < 64, "tile");
@@ -525,11 +579,11 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
                 load_to_lds(hr, b < XB ? (unsigned)(c * 8 + lrow) * XB + b : kOutOfRange,
                             lds + XAT + (unsigned)(h * XPLANE + c * 1024));
         }
-        load_to_lds(er, (unsigned)lane * 16u, lds + EAT);
-        if constexpr (BLOCK)
-            load4_to_lds(sr, (unsigned)is * 4u, lds + EAT + 1024u);
-        else if constexpr (scaled_rows(TYPE))
-            load4_to_lds(sr, lane < NB ? (unsigned)lane * 4u : kOutOfRange, lds + EAT + 1024u);
+        if (lane < BM)  // lane i writes at lds + 16 i (4 i), the others nothing
+            load_to_lds(er, (unsigned)lane * 16u, lds + EAT);
+        if constexpr (TYPE != kWBf16)
+            if (lane < NB)
+                load4_to_lds(sr, BLOCK ? (unsigned)is * 4u : (unsigned)lane * 4u, lds + SAT);
         if (++is == stages) {
             is = 0;
             if (++it < nt)
@@ -572,9 +626,9 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
             entry[j] = *reinterpret_cast<const u32x4 *>(st + EAT + r * 16);
         }
         if constexpr (BLOCK)
-            sc = *reinterpret_cast<const float *>(st + EAT + 1024 + lane * 4);
+            sc = *reinterpret_cast<const float *>(st + SAT);
         else if constexpr (scaled_rows(TYPE))
-            rows = *reinterpret_cast<const f32x4 *>(st + EAT + 1024 + (g * 4 % NB) * 4);
+            rows = *reinterpret_cast<const f32x4 *>(st + SAT + (g * 4 % NB) * 4);
         lds_read_wait();  // the stage is in registers: its slot may be written again
         if (s + RING < to)
             issue(slot);
@@ -748,28 +802,42 @@ __global__ __launch_bounds__(256) void experts_down_any_kernel(ExpertArgs a)
 namespace skg_host {
 namespace {
 
-// A launch holds fewer than 2^32 threads; blocks here have at most 512.
-constexpr int64_t kMaxBlocks = 1 << 22;
-
-// One tile height with its kernels: the first, for pairs of one wave or more, and the second,
-// for up to 16, 64 or 128 tokens.
+// The kernels for one tile height: the first, for pairs of one wave or more, and the second, for
+// 16 or 8 outputs a block, by the tokens that it has room for: up to 16, 64 or 128.
 struct ExpertsKernels {
-    const void *up[2], *down[3];
-    int up_features, down_features, up_waves, down_waves[3], rows;
+    const void *up[2], *down[2][3];
+    int rows, up_waves;
 };
+
+constexpr int kLds = 163840;
+
+// As many stages as fit, 6 at most.
+constexpr int ring_of(int bytes, int waves, int stage) { return bytes / (waves * stage) < 6 ? bytes / (waves * stage) : 6; }
+
+template <int TYPE, int BM, int WAVES, bool WAVE>
+const void *up_fn()
+{
+    constexpr int RING = ring_of(kLds - (int)sizeof(skg::Plan) - 64, WAVES, skg::up_stage<TYPE, BM>());
+    return (const void *)&skg::experts_up_kernel<TYPE, BM, RING, WAVES, WAVE>;
+}
+
+template <int TYPE, int NB, int BM, int MC>
+const void *down_fn()
+{
+    constexpr int WAVES = 8;
+    constexpr int RING = ring_of(kLds - 4 * skg::kMostTiles - WAVES * MC * NB * 4, WAVES, skg::down_stage<TYPE, NB, BM>());
+    return (const void *)&skg::experts_down_kernel<TYPE, NB, BM, RING, WAVES, MC>;
+}
 
 template <int TYPE, int BM>
 const ExpertsKernels &kernels_of()
 {
-    using namespace skg;
-    constexpr bool BYTES = TYPE != kWBf16;
-    constexpr int RU = BM == 32 && BYTES ? 1 : 2, R8 = BM == 8 ? 3 : 2, R4 = BM == 32 && BYTES ? 2 : 3;
-    static const ExpertsKernels k = {{(const void *)&experts_up_kernel<TYPE, 8, BM, RU, 8, false>,
-                                      (const void *)&experts_up_kernel<TYPE, 8, BM, RU, 8, true>},
-                                     {(const void *)&experts_down_kernel<TYPE, 16, BM, BM == 32 ? 1 : R8, 8, 16>,
-                                      (const void *)&experts_down_kernel<TYPE, 16, BM, R4, 4, 64>,
-                                      (const void *)&experts_down_kernel<TYPE, 16, BM, R4, 4, 128>},
-                                     8, 16, 8, {8, 4, 4}, BM};
+    constexpr int UW = BM == 32 && TYPE != skg::kWBf16 ? 4 : 8;
+    static const ExpertsKernels k = {
+        {up_fn<TYPE, BM, UW, false>(), up_fn<TYPE, BM, UW, true>()},
+        {{BM == 32 ? nullptr : down_fn<TYPE, 16, BM == 32 ? 16 : BM, 16>(), down_fn<TYPE, 16, BM, 64>(), nullptr},
+         {BM == 32 ? nullptr : down_fn<TYPE, 8, BM == 32 ? 16 : BM, 16>(), down_fn<TYPE, 8, BM, 64>(), down_fn<TYPE, 8, BM, 128>()}},
+        BM, UW};
     return k;
 }
 
@@ -780,18 +848,11 @@ const ExpertsKernels &kernels_for(int rows)
 }
 
 template <int TYPE>
-int run_type(const skg::ExpertArgs &a, bool vector, hipStream_t stream)
+int run_type(const skg::ExpertArgs &a, bool vector, int cus, hipStream_t stream)
 {
     using namespace skg;
     ExpertArgs args = a;
-    const int P = a.M * a.k;
-    // pairs of an expert that has any, were the pairs spread evenly
-    const double some = a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, P)), even = P / some;
-    const ExpertsKernels &k = kernels_for<TYPE>(even <= 4.0 ? 8 : even <= 10.0 ? 16 : 32);
-    int most = a.E + P / k.rows;  // tiles, at most
-    most = P < most ? P : most;
-    int nt = (a.I + k.up_features - 1) / k.up_features;
-    if (!vector || (int64_t)most * nt > kMaxBlocks) {
+    if (!vector) {
         void *p[] = {&args};
         const int64_t up = ((int64_t)a.M * a.k * a.I + 3) / 4, down = ((int64_t)a.M * a.H + 3) / 4;
         const int st = ops_launch((const void *)&experts_up_any_kernel<TYPE>, dim3((unsigned)(up < (1 << 20) ? up : 1 << 20)),
@@ -800,14 +861,20 @@ int run_type(const skg::ExpertArgs &a, bool vector, hipStream_t stream)
                                : ops_launch((const void *)&experts_down_any_kernel<TYPE>,
                                             dim3((unsigned)(down < (1 << 20) ? down : 1 << 20)), 256, p, stream);
     }
-    void *up[] = {&args, &nt};
-    const int st = ops_launch(k.up[P <= 64], dim3((unsigned)(1 + most * nt)), k.up_waves * 64, up, stream);
+    const int P = a.M * a.k;
+    // pairs of an expert that has any, were the pairs spread evenly
+    const double some = a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, P)), even = P / some;
+    const ExpertsKernels &k = kernels_for<TYPE>(even <= 4.0 ? 8 : even <= 10.0 || a.M <= 16 ? 16 : 32);
+    int most = a.E + P / k.rows;  // tiles, at most
+    most = P < most ? P : most;
+    void *up[] = {&args};
+    const int st = ops_launch(k.up[P <= 64], dim3((unsigned)cus), k.up_waves * 64, up, stream);
     if (st != SKINNY_OK)
         return st;
-    const int room = a.M <= 16 ? 0 : a.M <= 64 ? 1 : 2;
+    const int room = a.M <= 16 ? 0 : a.M <= 64 ? 1 : 2, narrow = room == 2 || a.H < 16 * cus;
     void *down[] = {&args, &most};
-    return ops_launch(k.down[room], dim3((unsigned)((a.H + k.down_features - 1) / k.down_features)), k.down_waves[room] * 64,
-                      down, stream);
+    const int nb = narrow ? 8 : 16;
+    return ops_launch(k.down[narrow][room], dim3((unsigned)((a.H + nb - 1) / nb)), 512, down, stream);
 }
 
 }  // namespace
@@ -866,16 +933,16 @@ int skinny_experts(const skinny_experts_t *e, hipStream_t stream)
         a.y = static_cast<uint16_t *>(e->y) + m * e->ldy;
         switch (e->type) {
         case SKINNY_WEIGHTS_BF16:
-            st = run_type<skg::kWBf16>(a, vector, stream);
+            st = run_type<skg::kWBf16>(a, vector, cus, stream);
             break;
         case SKINNY_WEIGHTS_E4M3_ROW:
-            st = run_type<skg::kWRow>(a, vector, stream);
+            st = run_type<skg::kWRow>(a, vector, cus, stream);
             break;
         case SKINNY_WEIGHTS_E4M3_BLOCK:
-            st = run_type<skg::kWBlock>(a, vector, stream);
+            st = run_type<skg::kWBlock>(a, vector, cus, stream);
             break;
         default:
-            st = run_type<skg::kWInt8>(a, vector, stream);
+            st = run_type<skg::kWInt8>(a, vector, cus, stream);
             break;
         }
         if (st != SKINNY_OK)
