@@ -53,7 +53,7 @@ struct ExpertArgs {
 };
 
 constexpr int kMostPairs = skg_host::kExpertsRows * skg_host::kMaxExpertsK;  // 4096: 12 bits and one
-constexpr int kMostTiles = skg_host::kMaxExperts + kMostPairs / 8;
+constexpr int kMostTiles = skg_host::kMaxExperts + kMostPairs / 4;
 static_assert(skg_host::kMaxExperts <= 1 << 10 && kMostPairs <= 1 << 15, "a tile is one word");
 
 // Sixteen 8-bit integers as bfloat16.
@@ -106,23 +106,26 @@ struct Fragment {
     }
 };
 
-// The lane's pieces of x that meet Fragment::v; `plane` bytes from one plane to the next.
-template <int TYPE>
-__device__ __forceinline__ void read_x(const uint8_t *row, int g, int swizzle, int plane, u32x4 (&v)[2 * planes<TYPE>()])
+// Rows of x (or h) in LDS: planes of [BM][128 bytes], whose 16-byte pieces are placed by the
+// row (with 4 rows a plane also by its parity), as the load instructions of 8 such rows do it.
+template <int BM>
+__device__ __forceinline__ int x_swizzle(int row, int plane) { return BM == 4 ? (row & 3) | (plane & 1) << 2 : row & 7; }
+
+// The lane's pieces of x that meet Fragment::v, of row `row` of the planes at `at`, the first
+// of which has the number `plane`.
+template <int TYPE, int BM>
+__device__ __forceinline__ void read_x(const uint8_t *at, int row, int plane, int g, u32x4 (&v)[2 * planes<TYPE>()])
 {
-    if constexpr (TYPE == kWBf16) {
-        v[0] = *reinterpret_cast<const u32x4 *>(row + (g ^ swizzle) * 16);
-        v[1] = *reinterpret_cast<const u32x4 *>(row + ((g + 4) ^ swizzle) * 16);
-    } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            v[q] = *reinterpret_cast<const u32x4 *>(row + (q / 2) * plane + ((2 * g + q % 2) ^ swizzle) * 16);
+    for (int q = 0; q < 2 * planes<TYPE>(); ++q) {
+        const int h = TYPE == kWBf16 ? 0 : q / 2, piece = TYPE == kWBf16 ? g + 4 * q : 2 * g + q % 2;
+        v[q] = *reinterpret_cast<const u32x4 *>(at + (h * BM + row) * 128 + (piece ^ x_swizzle<BM>(row, plane + h)) * 16);
     }
 }
 
 // Bytes of a stage: weights, x or h, and what belongs to them.
-template <int TYPE, int BM>
-constexpr int up_stage() { return 2048 + planes<TYPE>() * BM * 128 + (TYPE == kWBf16 ? 0 : 64); }
+template <int TYPE, int BM, bool RESIDENT>
+constexpr int up_stage() { return 2048 + (RESIDENT ? 0 : planes<TYPE>() * BM * 128) + (TYPE == kWBf16 ? 0 : 64); }
 template <int TYPE, int NB, int BM>
 constexpr int down_stage() { return NB * 128 + planes<TYPE>() * BM * 128 + BM * 16 + (TYPE == kWBf16 ? 0 : 64); }
 
@@ -130,9 +133,10 @@ constexpr int down_stage() { return NB * 128 + planes<TYPE>() * BM * 128 + BM * 
 
 // The plan of a pass in LDS, made by every block for itself: the tiles (expert | pairs << 10 |
 // first pair << 16) and each sorted pair's token.
+template <bool WAVE>
 struct Plan {
-    unsigned tiles[kMostTiles];
-    uint8_t tokens[kMostPairs];
+    unsigned tiles[WAVE ? 64 : kMostTiles];
+    uint8_t tokens[WAVE ? 64 : kMostPairs];
     int count;
 };
 
@@ -163,7 +167,7 @@ __device__ __forceinline__ void put_entry(const ExpertArgs &a, int at, int p)
 
 // Up to 64 pairs: the first wave sorts them in its lanes, by expert and then by pair.
 template <int BM>
-__device__ __forceinline__ void plan_wave(const ExpertArgs &a, int P, Plan &plan)
+__device__ __forceinline__ void plan_wave(const ExpertArgs &a, int P, Plan<true> &plan)
 {
     if (threadIdx.x >= 64)
         return;
@@ -201,7 +205,7 @@ __device__ __forceinline__ void plan_wave(const ExpertArgs &a, int P, Plan &plan
 // More: a bit for each token in a mask of each expert, so that a pair's place is the number of
 // bits before its own. Only where a token names an expert twice are pairs counted one by one.
 template <int BM, int THREADS>
-__device__ __forceinline__ void plan_block(const ExpertArgs &a, int P, Plan &plan, Scratch &s)
+__device__ __forceinline__ void plan_block(const ExpertArgs &a, int P, Plan<false> &plan, Scratch &s)
 {
     const int t = threadIdx.x;
     constexpr int WORDS = skg_host::kExpertsRows / 32;
@@ -280,25 +284,29 @@ __device__ __forceinline__ void plan_block(const ExpertArgs &a, int P, Plan &pla
 // ---- up ------------------------------------------------------------------------------
 
 // A unit is 8 features of both weights (16 rows of an instruction: gate, then up) for one
-// tile. Each block takes a run of units and each of its waves an equal run of their stages,
-// its loads going on from one unit to the next; only a unit that lies in several waves' runs
-// waits for the block's end, where its parts are added in the order of the waves. The
-// instruction's halves meet by an exchange of lanes, so a unit needs no barrier.
+// tile. Each block takes a run of units, tile by tile, and each of its waves an equal run of
+// their stages, its loads going on from one unit to the next; only a unit that lies in several
+// waves' runs waits for the tile's end, where its parts are added in the order of the waves.
+// The instruction's halves meet by an exchange of lanes, so a unit needs no barrier.
+// RESIDENT: the tile's rows of x stay in LDS (XROOM bytes of it), which leaves the ring to the
+// weights: what a unit streams is bound by the bytes in flight. Otherwise a stage holds its
+// part of them too.
 // WAVE: the pairs fit one wave.
-template <int TYPE, int BM, int RING, int WAVES, bool WAVE>
+template <int TYPE, int BM, int RING, int WAVES, bool WAVE, bool RESIDENT, int XROOM>
 __global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
 {
     constexpr bool BLOCK = TYPE == kWBlock;
     constexpr int PLANES = planes<TYPE>();
-    constexpr int TM = (BM + 15) / 16;
-    constexpr int XAT = 16 * 128, XPLANE = BM * 128, SAT = XAT + PLANES * XPLANE;
-    constexpr int STAGE = up_stage<TYPE, BM>();
-    constexpr int LOADS = 2 + PLANES * BM / 8 + (TYPE == kWBf16 ? 0 : 2);
-    constexpr int RINGS = WAVES * RING * STAGE;
-    constexpr int SMEM = !WAVE && (int)sizeof(Scratch) > RINGS ? (int)sizeof(Scratch) : RINGS;
-    static_assert(BM % 8 == 0 && BM <= 32 && (RING - 1) * LOADS < 64 && RING * STAGE >= TM * 1024, "tile");
+    constexpr int TM = (BM + 15) / 16, XR = (BM + 7) / 8;
+    constexpr int XAT = 16 * 128, XPLANE = BM * 128, SAT = XAT + (RESIDENT ? 0 : PLANES * XPLANE);
+    constexpr int STAGE = up_stage<TYPE, BM, RESIDENT>();
+    constexpr int LOADS = 2 + (RESIDENT ? 0 : PLANES * BM / 8) + (TYPE == kWBf16 ? 0 : 2);
+    constexpr int RINGS = WAVES * RING * STAGE, ROOM = RINGS + (RESIDENT ? XROOM : 0);
+    constexpr int SMEM = !WAVE && (int)sizeof(Scratch) > ROOM ? (int)sizeof(Scratch) : ROOM;
+    static_assert((BM == 4 || BM % 8 == 0) && BM <= 32 && RING * LOADS < 64 && RING * STAGE >= TM * 1024, "tile");
+    static_assert(RESIDENT || BM >= 8, "a stage's load of x takes 8 rows");
     __shared__ __attribute__((aligned(16))) uint8_t smem[SMEM];
-    __shared__ Plan plan;
+    __shared__ Plan<WAVE> plan;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -322,190 +330,212 @@ __global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
     const int nf = (a.I + 7) / 8, hb = (a.H + 127) / 128;
     const int64_t units = (int64_t)tiles * nf;
     const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-    const int64_t total = (u1 - u0) * stages;  // of the block
-    const int64_t from = total * wave / WAVES, to = total * (wave + 1) / WAVES;
-    const int n = (int)(to - from);  // stages of this wave
     const unsigned ldx = (unsigned)a.ldx * 2u, XB = (unsigned)a.H * 2u;
     const u32x4 xr = rsrc_words(a.x, (unsigned)(a.M - 1) * ldx + XB);
     uint8_t *ring = smem + wave * RING * STAGE;
-    const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem + wave * RING * STAGE;
+    const unsigned smem0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem;
+    const unsigned lds0 = smem0 + wave * RING * STAGE;
     const int lrow = lane >> 3;
     const unsigned piece = (unsigned)((lane & 7) ^ lrow) * 16u;
 
-    // the unit and stage that are loaded next
-    const int64_t begin = u0 + from / stages;
-    int it = (int)(begin / nf), iu = (int)(begin % nf), is = (int)(from % stages);
-    u32x4 wr[2], sr[2];
-    unsigned xat[BM / 8];  // the rows of x that this lane loads pieces of
-    auto enter_tile = [&] {
-        const unsigned v = __builtin_amdgcn_readfirstlane((int)plan.tiles[it]);
-        const int pairs = (int)(v >> 10 & 63u), first = (int)(v >> 16);
+    for (int64_t u = u0; u < u1;) {
+        const int t = (int)(u / nf), f0 = (int)(u % nf);
+        const int nu = (int)(u1 - u < nf - f0 ? u1 - u : nf - f0);  // units of this tile
+        u += nu;
+        const unsigned word = __builtin_amdgcn_readfirstlane((int)plan.tiles[t]);
+        const int e = (int)(word & 1023u), pairs = (int)(word >> 10 & 63u), first = (int)(word >> 16);
+        const int64_t total = (int64_t)nu * stages;
+        const int64_t from = total * wave / WAVES, to = total * (wave + 1) / WAVES;
+        const int n = (int)(to - from);  // stages of this wave
+
+        // the rows of x that this lane loads pieces of
+        unsigned xat[XR];
 #pragma unroll
-        for (int c = 0; c < BM / 8; ++c) {
-            const int r = c * 8 + lrow;
+        for (int c = 0; c < XR; ++c) {
+            const int r = BM == 4 ? lrow & 3 : c * 8 + lrow;
             xat[c] = r < pairs ? (unsigned)plan.tokens[first + r] * ldx : kOutOfRange;
         }
-    };
-    auto enter_unit = [&] {
-        const int e = (int)(__builtin_amdgcn_readfirstlane((int)plan.tiles[it]) & 1023u);
-        const int n0 = iu * 8, vn = a.I - n0 < 8 ? a.I - n0 : 8;
+        if constexpr (RESIDENT) {
+            constexpr int EACH = BM == 4 ? 2 : 1;  // planes of a load
+            const int all = stages * PLANES;  // with zeros behind x's end, where the weights have them too
+            for (int p = wave * EACH; p < all; p += WAVES * EACH) {
+                const unsigned b = (unsigned)(p + (BM == 4 ? lrow >> 2 : 0)) * 128u + piece;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            wr[q] = rsrc_words(a.w[q] + e * a.up_bytes + (int64_t)n0 * KB, (unsigned)vn * (unsigned)KB);
-            if constexpr (BLOCK)
-                sr[q] = rsrc_words(a.s[q] + e * a.up_scales + (int64_t)(n0 / 128) * hb, (unsigned)hb * 4u);
-            else if constexpr (scaled_rows(TYPE))
-                sr[q] = rsrc_words(a.s[q] + e * a.up_scales + n0, (unsigned)vn * 4u);
-        }
-    };
-    auto issue = [&](int slot) {
-        const unsigned k = (unsigned)is * 128u + piece;
-        const unsigned lds = lds0 + (unsigned)(slot * STAGE);
-        const unsigned at = k < (unsigned)KB ? (unsigned)lrow * (unsigned)KB + k : kOutOfRange;
-        load_to_lds<true>(wr[0], at, lds);
-        load_to_lds<true>(wr[1], at, lds + 1024u);
-#pragma unroll
-        for (int h = 0; h < PLANES; ++h) {
-            const unsigned b = (unsigned)(is * PLANES + h) * 128u + piece;
-#pragma unroll
-            for (int c = 0; c < BM / 8; ++c)
-                load_to_lds(xr, b < XB && xat[c] != kOutOfRange ? xat[c] + b : kOutOfRange,
-                            lds + XAT + (unsigned)(h * XPLANE + c * 1024));
-        }
-        if constexpr (TYPE != kWBf16) {  // 8 floats of each weight: its features' scales, or the block's
-            const unsigned f = BLOCK ? (unsigned)is * 4u : (unsigned)(lane & 7) * 4u;
-            if (lane < 8) {
-                load4_to_lds(sr[0], f, lds + SAT);
-                load4_to_lds(sr[1], f, lds + SAT + 32u);
+                for (int c = 0; c < XR; ++c)
+                    load_to_lds(xr, b < XB && xat[c] != kOutOfRange ? xat[c] + b : kOutOfRange,
+                                smem0 + RINGS + (unsigned)(p * XPLANE + c * 1024));
             }
         }
-        if (++is == stages) {
-            is = 0;
-            if (++iu == nf) {
-                iu = 0;
-                if (++it < tiles)
-                    enter_tile();
-            }
-            if (it < tiles)
-                enter_unit();
-        }
-    };
 
-    f32x4 acc[TM], head[TM] = {}, scale = {1.0f, 1.0f, 1.0f, 1.0f};  // head: see below
-    auto clear = [&] {
+        int iu = f0 + (int)(from / stages), is = (int)(from % stages);  // what is loaded next
+        u32x4 wr[2], sr[2];
+        auto enter_unit = [&] {
+            const int n0 = iu * 8, vn = a.I - n0 < 8 ? a.I - n0 : 8;
 #pragma unroll
-        for (int j = 0; j < TM; ++j)
-            acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    };
-    clear();
-    // h of a whole unit: lanes 0..31 hold the gate's sums, 32..63 the up projection's
-    auto finish = [&](int t, int u) {
-        const unsigned v = __builtin_amdgcn_readfirstlane((int)plan.tiles[t]);
-        const int pairs = (int)(v >> 10 & 63u), first = (int)(v >> 16), f = u * 8 + (g & 1) * 4;
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            f32x4 z = acc[j], o;
-            if constexpr (scaled_rows(TYPE))
-                z *= scale;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[e] = __shfl_xor(z[e], 32, 64);
-            const int r = j * 16 + i16;
-            if (lane < 32 && r < pairs && f < a.I) {  // I is a multiple of 8: all four are there
-                z = activate4(z, a.act) * o;
-                *reinterpret_cast<u32x2 *>(a.h + (int64_t)(first + r) * a.I + f) =
-                    u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+            for (int q = 0; q < 2; ++q) {
+                wr[q] = rsrc_words(a.w[q] + e * a.up_bytes + (int64_t)n0 * KB, (unsigned)vn * (unsigned)KB);
+                if constexpr (BLOCK)
+                    sr[q] = rsrc_words(a.s[q] + e * a.up_scales + (int64_t)(n0 / 128) * hb, (unsigned)hb * 4u);
+                else if constexpr (scaled_rows(TYPE))
+                    sr[q] = rsrc_words(a.s[q] + e * a.up_scales + n0, (unsigned)vn * 4u);
             }
-        }
-    };
+        };
+        auto issue = [&](int slot) {
+            const unsigned k = (unsigned)is * 128u + piece;
+            const unsigned lds = lds0 + (unsigned)(slot * STAGE);
+            const unsigned at = k < (unsigned)KB ? (unsigned)lrow * (unsigned)KB + k : kOutOfRange;
+            load_to_lds<true>(wr[0], at, lds);
+            load_to_lds<true>(wr[1], at, lds + 1024u);
+            if constexpr (!RESIDENT) {
+#pragma unroll
+                for (int h = 0; h < PLANES; ++h) {
+                    const unsigned b = (unsigned)(is * PLANES + h) * 128u + piece;
+#pragma unroll
+                    for (int c = 0; c < XR; ++c)
+                        load_to_lds(xr, b < XB && xat[c] != kOutOfRange ? xat[c] + b : kOutOfRange,
+                                    lds + XAT + (unsigned)(h * XPLANE + c * 1024));
+                }
+            }
+            if constexpr (TYPE != kWBf16) {  // 8 floats of each weight: its features' scales, or the block's
+                const unsigned f = BLOCK ? (unsigned)is * 4u : (unsigned)(lane & 7) * 4u;
+                if (lane < 8) {  // lane i writes at lds + 4 i, the others nothing
+                    load4_to_lds(sr[0], f, lds + SAT);
+                    load4_to_lds(sr[1], f, lds + SAT + 32u);
+                }
+            }
+            if (++is == stages) {
+                is = 0;
+                if (++iu < f0 + nu)
+                    enter_unit();
+            }
+        };
 
-    // the unit and stage that are multiplied next, and whether its sums began in this wave
-    int ct = it, cu = iu, cs = is;
-    bool whole = cs == 0;
-    if (n > 0) {
-        enter_tile();
-        enter_unit();
-#pragma unroll
-        for (int d = 0; d < RING; ++d)
-            if (d < n)
-                issue(d);
-    }
-    int slot = 0;
-    for (int s = 0; s < n; ++s) {
-        if (s + RING <= n)
-            stage_wait<(RING - 1) * LOADS>();
-        else
-            stage_wait<0>();
-        const uint8_t *st = ring + slot * STAGE;
-        Fragment<TYPE> af;
-        u32x4 bf[TM][2 * PLANES];
-        float sc = 1.0f;
-        const bool end = ++cs == stages;
-        af.read(st + i16 * 128, g, i16 & 7);
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            const int r = BM == 8 ? i16 & 7 : j * 16 + i16;
-            read_x<TYPE>(st + XAT + r * 128, g, r & 7, XPLANE, bf[j]);
-        }
-        if constexpr (BLOCK)
-            sc = *reinterpret_cast<const float *>(st + SAT + (g >> 1) * 32);
-        else if constexpr (scaled_rows(TYPE))
-            scale = *reinterpret_cast<const f32x4 *>(st + SAT + g * 16);
-        lds_read_wait();  // the stage is in registers: its slot may be written again
-        if (s + RING < n)
-            issue(slot);
-        slot = slot + 1 == RING ? 0 : slot + 1;
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            f32x4 p = BLOCK ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[j];
-#pragma unroll
-            for (int q = 0; q < 2 * PLANES; ++q)
-                p = mfma_bf16(af.v[q], bf[j][q], p);
-            if constexpr (BLOCK) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[j][e] = __builtin_fmaf(p[e], sc, acc[j][e]);
-            } else {
-                acc[j] = p;
-            }
-        }
-        if (end) {
-            cs = 0;
-            if (whole) {
-                finish(ct, cu);
-            } else {  // the end of a unit that an earlier wave began: the rest of its ring is
-                      // still being loaded, so the sums wait in registers
-#pragma unroll
-                for (int j = 0; j < TM; ++j)
-                    head[j] = acc[j];
-            }
-            whole = true;
-            clear();
-            if (++cu == nf) {
-                cu = 0;
-                ++ct;
-            }
-        }
-    }
-    // Units in several runs: a wave whose run began inside one leaves that part of its sums, and
-    // the wave that began it adds them up.
-    const bool inside = from % stages != 0;             // the run began inside a unit
-    const bool through = inside && !whole;              // and did not reach its end
-#pragma unroll
-    for (int j = 0; j < TM; ++j)
-        if (inside)
-            *reinterpret_cast<f32x4 *>(ring + (j * 64 + lane) * 16) = through ? acc[j] : head[j];
-    __syncthreads();
-    if (n > 0 && whole && cs != 0) {
-        const int64_t unit_end = to - cs + stages;
-        for (int w = wave + 1; w < WAVES; ++w) {
+        f32x4 acc[TM], head[TM], scale = {1.0f, 1.0f, 1.0f, 1.0f};  // head: see below
+        auto clear = [&] {
 #pragma unroll
             for (int j = 0; j < TM; ++j)
-                acc[j] += *reinterpret_cast<const f32x4 *>(smem + w * RING * STAGE + (j * 64 + lane) * 16);
-            if (total * (w + 1) / WAVES >= unit_end)
-                break;
+                acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        };
+        clear();
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+            head[j] = acc[j];
+        // h of a whole unit: lanes 0..31 hold the gate's sums, 32..63 the up projection's
+        auto finish = [&](int unit) {
+            const int f = unit * 8 + (g & 1) * 4;
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                f32x4 z = acc[j], o;
+                if constexpr (scaled_rows(TYPE))
+                    z *= scale;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    o[q] = __shfl_xor(z[q], 32, 64);
+                const int r = j * 16 + i16;
+                if (lane < 32 && r < pairs && f < a.I) {  // I is a multiple of 8: all four are there
+                    z = activate4(z, a.act) * o;
+                    *reinterpret_cast<u32x2 *>(a.h + (int64_t)(first + r) * a.I + f) =
+                        u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+                }
+            }
+        };
+
+        // the unit and stage that are multiplied next, and whether its sums began in this wave
+        int cu = iu, cs = is;
+        bool whole = cs == 0;
+        if (n > 0) {
+            enter_unit();
+#pragma unroll
+            for (int d = 0; d < RING; ++d)
+                if (d < n)
+                    issue(d);
         }
-        finish(ct, cu);
+        if constexpr (RESIDENT) {  // x has landed, here and in the other waves
+            if (n >= RING)
+                stage_wait<RING * LOADS>();
+            else
+                stage_wait<0>();
+            __syncthreads();
+        }
+        int slot = 0;
+        for (int s = 0; s < n; ++s) {
+            if (s + RING <= n)
+                stage_wait<(RING - 1) * LOADS>();
+            else
+                stage_wait<0>();
+            const uint8_t *st = ring + slot * STAGE;
+            Fragment<TYPE> af;
+            u32x4 bf[TM][2 * PLANES];
+            float sc = 1.0f;
+            af.read(st + i16 * 128, g, i16 & 7);
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                const int r = BM <= 8 ? i16 % BM : j * 16 + i16;
+                if constexpr (RESIDENT)
+                    read_x<TYPE, BM>(smem + RINGS + cs * PLANES * XPLANE, r, cs * PLANES, g, bf[j]);
+                else
+                    read_x<TYPE, BM>(st + XAT, r, 0, g, bf[j]);
+            }
+            if constexpr (BLOCK)
+                sc = *reinterpret_cast<const float *>(st + SAT + (g >> 1) * 32);
+            else if constexpr (scaled_rows(TYPE))
+                scale = *reinterpret_cast<const f32x4 *>(st + SAT + g * 16);
+            lds_read_wait();  // the stage is in registers: its slot may be written again
+            if (s + RING < n)
+                issue(slot);
+            slot = slot + 1 == RING ? 0 : slot + 1;
+#pragma unroll
+            for (int j = 0; j < TM; ++j) {
+                f32x4 p = BLOCK ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[j];
+#pragma unroll
+                for (int q = 0; q < 2 * PLANES; ++q)
+                    p = mfma_bf16(af.v[q], bf[j][q], p);
+                if constexpr (BLOCK) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        acc[j][q] = __builtin_fmaf(p[q], sc, acc[j][q]);
+                } else {
+                    acc[j] = p;
+                }
+            }
+            if (++cs == stages) {
+                cs = 0;
+                if (whole) {
+                    finish(cu);
+                } else {  // the end of a unit that an earlier wave began: its ring is still
+                          // being written, so the sums wait in registers
+#pragma unroll
+                    for (int j = 0; j < TM; ++j)
+                        head[j] = acc[j];
+                }
+                whole = true;
+                clear();
+                ++cu;
+            }
+        }
+
+        // Units in several runs: a wave whose run began inside one leaves that part of its
+        // sums, and the wave that began it adds them up.
+        const bool inside = from % stages != 0;  // the run began inside a unit
+        const bool through = inside && !whole;   // and did not reach its end
+        if (inside)
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+                *reinterpret_cast<f32x4 *>(ring + (j * 64 + lane) * 16) = through ? acc[j] : head[j];
+        __syncthreads();
+        if (n > 0 && whole && cs != 0) {
+            const int64_t unit_end = to - cs + stages;
+            for (int w = wave + 1; w < WAVES; ++w) {
+#pragma unroll
+                for (int j = 0; j < TM; ++j)
+                    acc[j] += *reinterpret_cast<const f32x4 *>(smem + w * RING * STAGE + (j * 64 + lane) * 16);
+                if (total * (w + 1) / WAVES >= unit_end)
+                    break;
+            }
+            finish(cu);
+        }
+        if (u < u1)
+            __syncthreads();  // the next tile is written over x and the parts
     }
 }
 
@@ -520,9 +550,10 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
     constexpr int TM = (BM + 15) / 16;
     constexpr int XAT = NB * 128, XPLANE = BM * 128, EAT = XAT + PLANES * XPLANE, SAT = EAT + BM * 16;
     constexpr int STAGE = down_stage<TYPE, NB, BM>();
-    constexpr int LOADS = NB / 8 + PLANES * BM / 8 + 1 + (TYPE == kWBf16 ? 0 : 1);
+    constexpr int HLOADS = BM == 4 ? 1 : PLANES * BM / 8;  // 8 rows each: with 4 rows both planes at once
+    constexpr int LOADS = NB / 8 + HLOADS + 1 + (TYPE == kWBf16 ? 0 : 1);
     constexpr int OUTS = MC * NB;  // floats of a wave
-    static_assert((NB == 8 || NB == 16) && BM % 8 == 0 && BM <= 32 && (RING - 1) * LOADS < 64, "tile");
+    static_assert((NB == 8 || NB == 16) && (BM == 4 || BM % 8 == 0) && BM <= 32 && (RING - 1) * LOADS < 64, "tile");
     __shared__ __attribute__((aligned(16))) uint8_t smem[WAVES * RING * STAGE];
     __shared__ __attribute__((aligned(16))) float outs[WAVES * OUTS];
     __shared__ unsigned tiles[kMostTiles];
@@ -571,13 +602,20 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
         for (int c = 0; c < NB / 8; ++c)
             load_to_lds<true>(wr, k < (unsigned)KB ? (unsigned)(c * 8 + lrow) * (unsigned)KB + k : kOutOfRange,
                               lds + (unsigned)c * 1024u);
+        // rows beyond the tile's lie beyond the resource
+        if constexpr (BM == 4) {
+            const unsigned b = (unsigned)(is * PLANES + (PLANES == 2 ? lrow >> 2 : 0)) * 128u + piece;
+            if (PLANES == 2 || lane < 32)
+                load_to_lds(hr, b < XB ? (unsigned)(lrow & 3) * XB + b : kOutOfRange, lds + XAT);
+        } else {
 #pragma unroll
-        for (int h = 0; h < PLANES; ++h) {
-            const unsigned b = (unsigned)(is * PLANES + h) * 128u + piece;
+            for (int h = 0; h < PLANES; ++h) {
+                const unsigned b = (unsigned)(is * PLANES + h) * 128u + piece;
 #pragma unroll
-            for (int c = 0; c < BM / 8; ++c)  // rows beyond the tile's lie beyond the resource
-                load_to_lds(hr, b < XB ? (unsigned)(c * 8 + lrow) * XB + b : kOutOfRange,
-                            lds + XAT + (unsigned)(h * XPLANE + c * 1024));
+                for (int c = 0; c < BM / 8; ++c)
+                    load_to_lds(hr, b < XB ? (unsigned)(c * 8 + lrow) * XB + b : kOutOfRange,
+                                lds + XAT + (unsigned)(h * XPLANE + c * 1024));
+            }
         }
         if (lane < BM)  // lane i writes at lds + 16 i (4 i), the others nothing
             load_to_lds(er, (unsigned)lane * 16u, lds + EAT);
@@ -621,8 +659,8 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
         af.read(st + (NB == 8 ? i16 & 7 : i16) * 128, g, i16 & 7);
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
-            const int r = BM == 8 ? i16 & 7 : j * 16 + i16;
-            read_x<TYPE>(st + XAT + r * 128, g, r & 7, XPLANE, bf[j]);
+            const int r = BM <= 8 ? i16 % BM : j * 16 + i16;
+            read_x<TYPE, BM>(st + XAT, r, 0, g, bf[j]);
             entry[j] = *reinterpret_cast<const u32x4 *>(st + EAT + r * 16);
         }
         if constexpr (BLOCK)
@@ -802,11 +840,12 @@ __global__ __launch_bounds__(256) void experts_down_any_kernel(ExpertArgs a)
 namespace skg_host {
 namespace {
 
-// The kernels for one tile height: the first, for pairs of one wave or more, and the second, for
-// 16 or 8 outputs a block, by the tokens that it has room for: up to 16, 64 or 128.
-struct ExpertsKernels {
-    const void *up[2], *down[2][3];
-    int rows, up_waves;
+// The kernels for one tile height: the first, for pairs of one wave or more, with x in LDS or
+// not (and the room that it takes), and the second, for 16 or 8 outputs a block, by the tokens
+// that it has room for: up to 16, 64 or 128.
+struct UpKernel {
+    const void *fn;
+    int waves, room;
 };
 
 constexpr int kLds = 163840;
@@ -814,11 +853,31 @@ constexpr int kLds = 163840;
 // As many stages as fit, 6 at most.
 constexpr int ring_of(int bytes, int waves, int stage) { return bytes / (waves * stage) < 6 ? bytes / (waves * stage) : 6; }
 
-template <int TYPE, int BM, int WAVES, bool WAVE>
-const void *up_fn()
+template <int TYPE, int BM, bool WAVE, int RING>
+UpKernel up_resident()
 {
-    constexpr int RING = ring_of(kLds - (int)sizeof(skg::Plan) - 64, WAVES, skg::up_stage<TYPE, BM>());
-    return (const void *)&skg::experts_up_kernel<TYPE, BM, RING, WAVES, WAVE>;
+    constexpr int ROOM = (kLds - (int)sizeof(skg::Plan<WAVE>) - 64 - RING * 8 * skg::up_stage<TYPE, BM, true>()) / 1024 * 1024;
+    return UpKernel{(const void *)&skg::experts_up_kernel<TYPE, BM, RING, 8, WAVE, true, ROOM>, 8, ROOM};
+}
+
+template <int TYPE, int BM, bool WAVE>
+UpKernel up_streamed()
+{
+    constexpr int B = BM == 4 ? 8 : BM, WAVES = BM == 32 && TYPE != skg::kWBf16 ? 4 : 8;
+    constexpr int RING = ring_of(kLds - (int)sizeof(skg::Plan<WAVE>) - 64, WAVES, skg::up_stage<TYPE, B, false>());
+    return UpKernel{(const void *)&skg::experts_up_kernel<TYPE, B, RING, WAVES, WAVE, false, 0>, WAVES, 0};
+}
+
+// The first kernel for rows of `xbytes` bytes of x.
+template <int TYPE, int BM, bool WAVE>
+UpKernel up_kernel(int64_t xbytes)
+{
+    static const UpKernel k[] = {up_resident<TYPE, BM, WAVE, 6>(), up_resident<TYPE, BM, WAVE, 4>(),
+                                 up_resident<TYPE, BM, WAVE, 3>()};
+    for (const UpKernel &u : k)
+        if ((xbytes + 255) / 256 * 256 * BM <= u.room)
+            return u;
+    return up_streamed<TYPE, BM, WAVE>();
 }
 
 template <int TYPE, int NB, int BM, int MC>
@@ -830,21 +889,34 @@ const void *down_fn()
 }
 
 template <int TYPE, int BM>
-const ExpertsKernels &kernels_of()
+const void *down_kernel(int M, bool narrow)
 {
-    constexpr int UW = BM == 32 && TYPE != skg::kWBf16 ? 4 : 8;
-    static const ExpertsKernels k = {
-        {up_fn<TYPE, BM, UW, false>(), up_fn<TYPE, BM, UW, true>()},
-        {{BM == 32 ? nullptr : down_fn<TYPE, 16, BM == 32 ? 16 : BM, 16>(), down_fn<TYPE, 16, BM, 64>(), nullptr},
-         {BM == 32 ? nullptr : down_fn<TYPE, 8, BM == 32 ? 16 : BM, 16>(), down_fn<TYPE, 8, BM, 64>(), down_fn<TYPE, 8, BM, 128>()}},
-        BM, UW};
-    return k;
+    constexpr int B = BM == 32 ? 16 : BM;
+    if (M <= 16)  // tiles of 32 rows are for more
+        return narrow ? down_fn<TYPE, 8, B, 16>() : down_fn<TYPE, 16, B, 16>();
+    if (M <= 64)
+        return narrow ? down_fn<TYPE, 8, BM, 64>() : down_fn<TYPE, 16, BM, 64>();
+    return down_fn<TYPE, 8, BM, 128>();
 }
 
-template <int TYPE>
-const ExpertsKernels &kernels_for(int rows)
+// Both kernels with tiles of BM rows.
+template <int TYPE, int BM>
+int run_rows(skg::ExpertArgs &a, int cus, hipStream_t stream)
 {
-    return rows <= 8 ? kernels_of<TYPE, 8>() : rows <= 16 ? kernels_of<TYPE, 16>() : kernels_of<TYPE, 32>();
+    const int P = a.M * a.k;
+    const int64_t xbytes = 2 * (int64_t)a.H;
+    const UpKernel up = P <= 64 ? up_kernel<TYPE, BM, true>(xbytes) : up_kernel<TYPE, BM, false>(xbytes);
+    const int height = up.room ? BM : BM < 8 ? 8 : BM;
+    int most = a.E + P / height;  // tiles, at most
+    most = P < most ? P : most;
+    void *args[] = {&a, &most};
+    const int st = ops_launch(up.fn, dim3((unsigned)cus), up.waves * 64, args, stream);
+    if (st != SKINNY_OK)
+        return st;
+    const bool narrow = a.M > 64 || a.H < 16 * cus;
+    const void *down = height == BM ? down_kernel<TYPE, BM>(a.M, narrow) : down_kernel<TYPE, 8>(a.M, narrow);
+    const int nb = narrow ? 8 : 16;
+    return ops_launch(down, dim3((unsigned)(((int64_t)a.H + nb - 1) / nb)), 512, args, stream);
 }
 
 template <int TYPE>
@@ -864,17 +936,11 @@ int run_type(const skg::ExpertArgs &a, bool vector, int cus, hipStream_t stream)
     const int P = a.M * a.k;
     // pairs of an expert that has any, were the pairs spread evenly
     const double some = a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, P)), even = P / some;
-    const ExpertsKernels &k = kernels_for<TYPE>(even <= 4.0 ? 8 : even <= 10.0 || a.M <= 16 ? 16 : 32);
-    int most = a.E + P / k.rows;  // tiles, at most
-    most = P < most ? P : most;
-    void *up[] = {&args};
-    const int st = ops_launch(k.up[P <= 64], dim3((unsigned)cus), k.up_waves * 64, up, stream);
-    if (st != SKINNY_OK)
-        return st;
-    const int room = a.M <= 16 ? 0 : a.M <= 64 ? 1 : 2, narrow = room == 2 || a.H < 16 * cus;
-    void *down[] = {&args, &most};
-    const int nb = narrow ? 8 : 16;
-    return ops_launch(k.down[narrow][room], dim3((unsigned)((a.H + nb - 1) / nb)), 512, down, stream);
+    const int rows = even <= 2.0 ? 4 : even <= 7.0 ? 8 : even <= 12.0 || a.M <= 16 ? 16 : 32;
+    return rows == 4    ? run_rows<TYPE, 4>(args, cus, stream)
+           : rows == 8  ? run_rows<TYPE, 8>(args, cus, stream)
+           : rows == 16 ? run_rows<TYPE, 16>(args, cus, stream)
+                        : run_rows<TYPE, 32>(args, cus, stream);
 }
 
 }  // namespace

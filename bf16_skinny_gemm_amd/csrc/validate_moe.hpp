@@ -66,7 +66,7 @@ inline ExpertsSpace experts_space(int32_t M, int32_t k, int32_t E, int32_t I)
 {
     const uint64_t pairs = (uint64_t)(M < kExpertsRows ? M : kExpertsRows) * (uint64_t)k;
     // every expert may have a tile that is not full
-    const uint64_t most = pairs < (uint64_t)E + pairs / 8 ? pairs : (uint64_t)E + pairs / 8;
+    const uint64_t most = pairs < (uint64_t)E + pairs / 4 ? pairs : (uint64_t)E + pairs / 4;
     ExpertsSpace s{};
     s.tiles = 16;
     s.entries = s.tiles + (4 * most + 15) / 16 * 16;
