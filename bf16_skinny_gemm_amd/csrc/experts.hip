@@ -9,13 +9,14 @@
 // ring of stages of 128 bytes of K in LDS, filled by loads that write LDS, and waits for its
 // own loads only.
 //
-//  - up: one block per tile and NB features of both weights. K = H is split over its
-//    waves, whose sums meet in LDS at the end.
-//  - down: one block per NB outputs of all tokens. Each wave takes a run of the stages of
-//    all tiles, one after the other, so its loads go on from one expert to the next; behind
-//    a tile it adds its sums, times the token's weight, to its own outputs [tokens][NB] in
-//    LDS. The waves' outputs are added in the order of the waves: no atomics, the same bits
-//    every time.
+//  - up: 8 features of both weights for one tile at a time; every block takes an equal run of
+//    them.
+//  - down: 16 outputs of all tokens at a time, for each of them the stages of all tiles; every
+//    block takes an equal run of all that. Of its part of 16 outputs, each wave takes a run of
+//    stages, so its loads go on from one expert to the next; behind a tile it adds its sums,
+//    times the token's weight, to its own outputs [tokens][16] in LDS. The waves' outputs
+//    are added in the order of the waves, and where several blocks share 16 outputs, their
+//    parts in the order of the blocks by the one that ends last: the same bits every time.
 //
 // 8-bit weights are widened to bfloat16 (exactly) and multiplied by x as it is, so that only
 // h and y are rounded: at 16 rows a tile, the matrix instructions cost nothing.
@@ -35,6 +36,15 @@ enum { kWBf16 = SKINNY_WEIGHTS_BF16, kWRow = SKINNY_WEIGHTS_E4M3_ROW, kWBlock = 
        kWInt8 = SKINNY_WEIGHTS_INT8_ROW };
 constexpr bool scaled_rows(int type) { return type == kWRow || type == kWInt8; }
 
+// Division of x < 2^31 by a number that the host knows: (x + high word of mul x) >> shift, with
+// mul = floor(2^32 (2^shift - d) / d) + 1 and 2^shift the least power >= d (Granlund and
+// Montgomery). Six divisions at run time took 1.4 us of a launch.
+struct Divisor {
+    unsigned mul, shift;
+
+    __device__ __forceinline__ int of(int x) const { return (int)((__umulhi(mul, (unsigned)x) + (unsigned)x) >> shift); }
+};
+
 struct ExpertArgs {
     const uint16_t *x;
     const int *ids;
@@ -43,13 +53,18 @@ struct ExpertArgs {
     const float *s[2], *sd;     // their scales
     const uint16_t *res;        // or null
     uint16_t *y, *h;
-    unsigned *plan;             // [0] tiles; from [4]: expert | pairs << 10 | first pair << 16 of each
+    unsigned *plan;             // [0] tiles, [1..3] the second kernel's Runs; from [4], of each tile:
+                                // expert | pairs << 10 | first pair << 16
     u32x4 *entries;             // for each pair, by expert: token, its weight
+    u32x4 *begins;              // of the second kernel's blocks: set of outputs, stage, stages in all
+    unsigned *arrived;          // see there
+    float *parts;
     int64_t ldx, ldr, ldy;      // elements
     int64_t up_bytes, down_bytes;  // from one expert's weight to the next
     int64_t up_scales, down_scales;
     int M, E, k, H, I;
     int act;
+    Divisor by_k, by_grid, by_features, by_up, by_down;  // k, blocks, I / 8, the stages of H and of I
 };
 
 constexpr int kMostPairs = skg_host::kExpertsRows * skg_host::kMaxExpertsK;  // 4096: 12 bits and one
@@ -126,8 +141,8 @@ __device__ __forceinline__ void read_x(const uint8_t *at, int row, int plane, in
 // Bytes of a stage: weights, x or h, and what belongs to them.
 template <int TYPE, int BM, bool RESIDENT>
 constexpr int up_stage() { return 2048 + (RESIDENT ? 0 : planes<TYPE>() * BM * 128) + (TYPE == kWBf16 ? 0 : 64); }
-template <int TYPE, int NB, int BM>
-constexpr int down_stage() { return NB * 128 + planes<TYPE>() * BM * 128 + BM * 16 + (TYPE == kWBf16 ? 0 : 64); }
+template <int TYPE, int BM>
+constexpr int down_stage() { return 2048 + planes<TYPE>() * BM * 128 + BM * 16 + (TYPE == kWBf16 ? 0 : 64); }
 
 // ---- the pairs by expert -----------------------------------------------------------
 
@@ -162,7 +177,7 @@ __device__ __forceinline__ int wave_scan(int v)
 
 __device__ __forceinline__ void put_entry(const ExpertArgs &a, int at, int p)
 {
-    a.entries[at] = u32x4{(unsigned)(p / a.k), __builtin_bit_cast(unsigned, a.weights[p]), 0, 0};
+    a.entries[at] = u32x4{(unsigned)a.by_k.of(p), __builtin_bit_cast(unsigned, a.weights[p]), 0, 0};
 }
 
 // Up to 64 pairs: the first wave sorts them in its lanes, by expert and then by pair.
@@ -191,7 +206,7 @@ __device__ __forceinline__ void plan_wave(const ExpertArgs &a, int P, Plan<true>
         before += o < pos;
     }
     if (in) {
-        plan.tokens[pos] = (uint8_t)(lane / a.k);
+        plan.tokens[pos] = (uint8_t)a.by_k.of(lane);
         if (blockIdx.x == 0)
             put_entry(a, pos, lane);
     }
@@ -215,7 +230,7 @@ __device__ __forceinline__ void plan_block(const ExpertArgs &a, int P, Plan<fals
         s.twice = 0;
     __syncthreads();
     for (int p = t; p < P; p += THREADS) {
-        const int id = a.ids[p], m = p / a.k;
+        const int id = a.ids[p], m = a.by_k.of(p);
         const bool in = (unsigned)id < (unsigned)a.E;
         s.ids[p] = in ? (uint16_t)id : (uint16_t)0xFFFF;
         if (in && (atomicOr(&s.named[id][m / 32], 1u << (m % 32)) >> (m % 32) & 1))
@@ -263,7 +278,7 @@ __device__ __forceinline__ void plan_block(const ExpertArgs &a, int P, Plan<fals
             plan.tiles[tile + r / BM] = (unsigned)e | (unsigned)(n - r < BM ? n - r : BM) << 10 | (unsigned)(first + r) << 16;
     }
     for (int p = t; p < P; p += THREADS) {
-        const int e = s.ids[p], m = p / a.k;
+        const int e = s.ids[p], m = a.by_k.of(p);
         if (e == 0xFFFF)
             continue;
         int at = s.first[e];
@@ -278,6 +293,56 @@ __device__ __forceinline__ void plan_block(const ExpertArgs &a, int P, Plan<fals
         plan.tokens[at] = (uint8_t)m;
         if (blockIdx.x == 0)
             put_entry(a, at, p);
+    }
+}
+
+// ---- runs ------------------------------------------------------------------------------
+
+// A line of things in `runs` runs of sizes that differ by one at most: the first `more` runs have
+// per + 1 things.
+struct Runs {
+    unsigned runs, per, more;
+
+    __device__ __forceinline__ unsigned start(unsigned r) const { return r * per + (r < more ? r : more); }
+    __device__ __forceinline__ unsigned of(unsigned at) const
+    {
+        const unsigned head = more * (per + 1);
+        return at < head ? at / (per + 1) : more + (at - head) / per;
+    }
+};
+
+// `all` things in at most `most` = gridDim.x runs, none of them empty.
+__device__ __forceinline__ Runs runs_of(unsigned all, unsigned most, const Divisor &by_most)
+{
+    if (all <= most)
+        return Runs{all, 1, 0};
+    const unsigned per = (unsigned)by_most.of((int)all);
+    return Runs{most, per, all - per * most};
+}
+
+// What the second kernel's blocks take: nj sets of 16 outputs with T stages each, in one line.
+// Up to kWhole stages are worth less than what blocks that share a set pay for it: then the
+// runs are of whole sets.
+constexpr int kWhole = 64;
+constexpr int per_stage(int type) { return type == kWBf16 ? 64 : 128; }
+
+template <int TYPE, int THREADS>
+__device__ __forceinline__ void write_runs(const ExpertArgs &a, int tiles)
+{
+    const int nj = (a.H + 15) / 16, T = tiles * ((a.I + per_stage(TYPE) - 1) / per_stage(TYPE));
+    if (T == 0)
+        return;
+    const int unit = T <= kWhole ? T : 1;
+    const unsigned all = (unsigned)(nj * (T / unit)), runs = all < skg_host::kDownBlocks ? all : skg_host::kDownBlocks;
+    const Runs share{runs, all / runs, all % runs};
+    if (threadIdx.x == 0) {
+        a.plan[1] = share.runs;
+        a.plan[2] = share.per;
+        a.plan[3] = share.more;
+    }
+    for (unsigned b = threadIdx.x; b < runs; b += THREADS) {
+        const unsigned w0 = share.start(b) * unit, w1 = share.start(b + 1) * unit;
+        a.begins[b] = u32x4{w0 / T, w0 % T, w1 - w0, 0};
     }
 }
 
@@ -319,17 +384,22 @@ __global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
     __syncthreads();
     const int tiles = __builtin_amdgcn_readfirstlane(plan.count);
     if (blockIdx.x == 0) {  // for the second kernel
+        for (int i = threadIdx.x; i < skg_host::kDownBlocks; i += WAVES * 64)
+            a.arrived[i] = 0;
         for (int i = threadIdx.x; i < tiles; i += WAVES * 64)
             a.plan[4 + i] = plan.tiles[i];
         if (threadIdx.x == 0)
             a.plan[0] = (unsigned)tiles;
+        write_runs<TYPE, WAVES * 64>(a, tiles);
     }
 
     const int KB = TYPE == kWBf16 ? a.H * 2 : a.H;
     const int stages = (KB + 127) / 128;
     const int nf = (a.I + 7) / 8, hb = (a.H + 127) / 128;
-    const int64_t units = (int64_t)tiles * nf;
-    const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+    const Runs share = runs_of((unsigned)(tiles * nf), gridDim.x, a.by_grid);
+    if (blockIdx.x >= share.runs)
+        return;
+    const int u0 = (int)share.start(blockIdx.x), u1 = (int)share.start(blockIdx.x + 1);
     const unsigned ldx = (unsigned)a.ldx * 2u, XB = (unsigned)a.H * 2u;
     const u32x4 xr = rsrc_words(a.x, (unsigned)(a.M - 1) * ldx + XB);
     uint8_t *ring = smem + wave * RING * STAGE;
@@ -338,15 +408,15 @@ __global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
     const int lrow = lane >> 3;
     const unsigned piece = (unsigned)((lane & 7) ^ lrow) * 16u;
 
-    for (int64_t u = u0; u < u1;) {
-        const int t = (int)(u / nf), f0 = (int)(u % nf);
-        const int nu = (int)(u1 - u < nf - f0 ? u1 - u : nf - f0);  // units of this tile
+    for (int u = u0; u < u1;) {
+        const int t = a.by_features.of(u), f0 = u - t * nf;
+        const int nu = u1 - u < nf - f0 ? u1 - u : nf - f0;  // units of this tile
         u += nu;
         const unsigned word = __builtin_amdgcn_readfirstlane((int)plan.tiles[t]);
         const int e = (int)(word & 1023u), pairs = (int)(word >> 10 & 63u), first = (int)(word >> 16);
-        const int64_t total = (int64_t)nu * stages;
-        const int64_t from = total * wave / WAVES, to = total * (wave + 1) / WAVES;
-        const int n = (int)(to - from);  // stages of this wave
+        const unsigned total = (unsigned)(nu * stages);
+        auto start = [&](int w) { return (int)(total / WAVES * w + total % WAVES * w / WAVES); };
+        const int from = start(wave), to = start(wave + 1), n = to - from;  // stages of this wave
 
         // the rows of x that this lane loads pieces of
         unsigned xat[XR];
@@ -367,7 +437,8 @@ __global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
             }
         }
 
-        int iu = f0 + (int)(from / stages), is = (int)(from % stages);  // what is loaded next
+        const int skipped = a.by_up.of(from);  // units before the run
+        int iu = f0 + skipped, is = from - skipped * stages;  // what is loaded next
         u32x4 wr[2], sr[2];
         auto enter_unit = [&] {
             const int n0 = iu * 8, vn = a.I - n0 < 8 ? a.I - n0 : 8;
@@ -516,7 +587,7 @@ __global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
 
         // Units in several runs: a wave whose run began inside one leaves that part of its
         // sums, and the wave that began it adds them up.
-        const bool inside = from % stages != 0;  // the run began inside a unit
+        const bool inside = skipped * stages != from;  // the run began inside a unit
         const bool through = inside && !whole;   // and did not reach its end
         if (inside)
 #pragma unroll
@@ -524,12 +595,12 @@ __global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
                 *reinterpret_cast<f32x4 *>(ring + (j * 64 + lane) * 16) = through ? acc[j] : head[j];
         __syncthreads();
         if (n > 0 && whole && cs != 0) {
-            const int64_t unit_end = to - cs + stages;
+            const int unit_end = to - cs + stages;
             for (int w = wave + 1; w < WAVES; ++w) {
 #pragma unroll
                 for (int j = 0; j < TM; ++j)
                     acc[j] += *reinterpret_cast<const f32x4 *>(smem + w * RING * STAGE + (j * 64 + lane) * 16);
-                if (total * (w + 1) / WAVES >= unit_end)
+                if (start(w + 1) >= unit_end)
                     break;
             }
             finish(cu);
@@ -541,201 +612,259 @@ __global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
 
 // ---- down ----------------------------------------------------------------------------
 
+// s_waitcnt operand: vmcnt 0, the other counters left at their largest.
+constexpr int kWaitStores = 0x0F70;
+
 // MC: tokens that the block has room for.
-template <int TYPE, int NB, int BM, int RING, int WAVES, int MC>
+template <int TYPE, int BM, int RING, int WAVES, int MC>
 __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, int most_tiles)
 {
     constexpr bool BLOCK = TYPE == kWBlock;
     constexpr int PLANES = planes<TYPE>();
     constexpr int TM = (BM + 15) / 16;
-    constexpr int XAT = NB * 128, XPLANE = BM * 128, EAT = XAT + PLANES * XPLANE, SAT = EAT + BM * 16;
-    constexpr int STAGE = down_stage<TYPE, NB, BM>();
+    constexpr int XAT = 2048, XPLANE = BM * 128, EAT = XAT + PLANES * XPLANE, SAT = EAT + BM * 16;
+    constexpr int STAGE = down_stage<TYPE, BM>();
     constexpr int HLOADS = BM == 4 ? 1 : PLANES * BM / 8;  // 8 rows each: with 4 rows both planes at once
-    constexpr int LOADS = NB / 8 + HLOADS + 1 + (TYPE == kWBf16 ? 0 : 1);
-    constexpr int OUTS = MC * NB;  // floats of a wave
-    static_assert((NB == 8 || NB == 16) && (BM == 4 || BM % 8 == 0) && BM <= 32 && (RING - 1) * LOADS < 64, "tile");
+    constexpr int LOADS = 2 + HLOADS + 1 + (TYPE == kWBf16 ? 0 : 1);
+    constexpr int OUTS = MC * 16;  // floats of a wave
+    static_assert((BM == 4 || BM % 8 == 0) && BM <= 32 && (RING - 1) * LOADS < 64, "tile");
     __shared__ __attribute__((aligned(16))) uint8_t smem[WAVES * RING * STAGE];
     __shared__ __attribute__((aligned(16))) float outs[WAVES * OUTS];
     __shared__ unsigned tiles[kMostTiles];
+    __shared__ unsigned earlier;
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i16 = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * NB;
+    // one round trip for the plan: scalar loads would come behind the tiles'
+    int zero = 0;
+    asm volatile("" : "+v"(zero));
+    const u32x4 head = *reinterpret_cast<const u32x4 *>(a.plan + zero), run = a.begins[(int)blockIdx.x + zero];
     for (int i = threadIdx.x; i < most_tiles; i += WAVES * 64)
         tiles[i] = a.plan[4 + i];
-    const int nt = __builtin_amdgcn_readfirstlane((int)a.plan[0]);
+    const int nt = __builtin_amdgcn_readfirstlane((int)head[0]);
+    const Runs share{(unsigned)__builtin_amdgcn_readfirstlane((int)head[1]), (unsigned)__builtin_amdgcn_readfirstlane((int)head[2]),
+                     (unsigned)__builtin_amdgcn_readfirstlane((int)head[3])};
     float *out = outs + wave * OUTS;
-    for (int i = lane; i < a.M * NB / 4; i += 64)
-        reinterpret_cast<f32x4 *>(out)[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    __syncthreads();
 
     const int KB = TYPE == kWBf16 ? a.I * 2 : a.I;
     const unsigned XB = (unsigned)a.I * 2u;
     const int stages = (KB + 127) / 128, ib = (a.I + 127) / 128;
-    const int vn = a.H - n0 < NB ? a.H - n0 : NB;
-    const int total = nt * stages;
-    const int from = (int)((int64_t)total * wave / WAVES), to = (int)((int64_t)total * (wave + 1) / WAVES);
     const uint8_t *ring = smem + wave * RING * STAGE;
     const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)smem + wave * RING * STAGE;
     const int lrow = lane >> 3;
     const unsigned piece = (unsigned)((lane & 7) ^ lrow) * 16u;
 
-    // the tile and stage that are loaded next
-    int it = from < to ? from / stages : 0, is = from < to ? from % stages : 0;
-    u32x4 wr, hr, er, sr;
-    auto enter = [&](int t) {
-        const unsigned v = __builtin_amdgcn_readfirstlane((int)tiles[t]);
-        const int e = (int)(v & 1023u), pairs = (int)(v >> 10 & 63u), first = (int)(v >> 16);
-        wr = rsrc_words(a.wd + e * a.down_bytes + (int64_t)n0 * KB, (unsigned)vn * (unsigned)KB);
-        hr = rsrc_words(a.h + (int64_t)first * a.I, (unsigned)pairs * XB);
-        er = rsrc_words(a.entries + first, (unsigned)pairs * 16u);
-        if constexpr (BLOCK)
-            sr = rsrc_words(a.sd + e * a.down_scales + (int64_t)(n0 / 128) * ib, (unsigned)ib * 4u);
-        else if constexpr (scaled_rows(TYPE))
-            sr = rsrc_words(a.sd + e * a.down_scales + n0, (unsigned)vn * 4u);
-    };
-    auto issue = [&](int slot) {
-        const unsigned k = (unsigned)is * 128u + piece;
-        const unsigned lds = lds0 + (unsigned)(slot * STAGE);
-#pragma unroll
-        for (int c = 0; c < NB / 8; ++c)
-            load_to_lds<true>(wr, k < (unsigned)KB ? (unsigned)(c * 8 + lrow) * (unsigned)KB + k : kOutOfRange,
-                              lds + (unsigned)c * 1024u);
-        // rows beyond the tile's lie beyond the resource
-        if constexpr (BM == 4) {
-            const unsigned b = (unsigned)(is * PLANES + (PLANES == 2 ? lrow >> 2 : 0)) * 128u + piece;
-            if (PLANES == 2 || lane < 32)
-                load_to_lds(hr, b < XB ? (unsigned)(lrow & 3) * XB + b : kOutOfRange, lds + XAT);
-        } else {
-#pragma unroll
-            for (int h = 0; h < PLANES; ++h) {
-                const unsigned b = (unsigned)(is * PLANES + h) * 128u + piece;
-#pragma unroll
-                for (int c = 0; c < BM / 8; ++c)
-                    load_to_lds(hr, b < XB ? (unsigned)(c * 8 + lrow) * XB + b : kOutOfRange,
-                                lds + XAT + (unsigned)(h * XPLANE + c * 1024));
-            }
-        }
-        if (lane < BM)  // lane i writes at lds + 16 i (4 i), the others nothing
-            load_to_lds(er, (unsigned)lane * 16u, lds + EAT);
-        if constexpr (TYPE != kWBf16)
-            if (lane < NB)
-                load4_to_lds(sr, BLOCK ? (unsigned)is * 4u : (unsigned)lane * 4u, lds + SAT);
-        if (++is == stages) {
-            is = 0;
-            if (++it < nt)
-                enter(it);
-        }
+    // four outputs of a token, from their sum
+    auto store = [&](int o, int n0, f32x4 v) {
+        const int m = o / 4, n = n0 + o % 4 * 4;
+        if (n >= a.H)
+            return;  // H is a multiple of 8: all four are there or none
+        if (a.res)
+            v += widen4(*reinterpret_cast<const u32x2_any *>(a.res + m * a.ldr + n));
+        *reinterpret_cast<u32x2_any *>(a.y + m * a.ldy + n) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
     };
 
-    f32x4 acc[TM];
-    auto clear = [&] {
-#pragma unroll
-        for (int j = 0; j < TM; ++j)
-            acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    };
-    clear();
-    int ct = it, cs = is;  // the tile and stage that are multiplied next
-    if (from < to) {
-        enter(it);
-#pragma unroll
-        for (int d = 0; d < RING; ++d)
-            if (from + d < to)
-                issue(d);
+    const int nj = (a.H + 15) / 16, T = nt * stages;
+    if (T == 0) {  // no pair names an expert
+        for (int j = blockIdx.x; j < nj; j += gridDim.x)
+            for (int o = threadIdx.x; o < a.M * 4; o += WAVES * 64)
+                store(o, j * 16, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        return;
     }
-    int slot = 0;
-    for (int s = from; s < to; ++s) {
-        if (s + RING <= to)
-            stage_wait<(RING - 1) * LOADS>();
-        else
-            stage_wait<0>();
-        const uint8_t *st = ring + slot * STAGE;
-        Fragment<TYPE> af;
-        u32x4 bf[TM][2 * PLANES], entry[TM];
-        float sc = 1.0f;
-        f32x4 rows = {1.0f, 1.0f, 1.0f, 1.0f};
-        const bool last = ++cs == stages || s + 1 == to;
-        af.read(st + (NB == 8 ? i16 & 7 : i16) * 128, g, i16 & 7);
+    if (blockIdx.x >= share.runs)
+        return;
+    int j = __builtin_amdgcn_readfirstlane((int)run[0]), begin = __builtin_amdgcn_readfirstlane((int)run[1]);
+    int left = __builtin_amdgcn_readfirstlane((int)run[2]);
+    for (; left > 0; ++j, begin = 0) {
+        const int len = left < T - begin ? left : T - begin;
+        left -= len;
+        const int n0 = j * 16, vn = a.H - n0 < 16 ? a.H - n0 : 16;
+        const int from = begin + len / WAVES * wave + len % WAVES * wave / WAVES;
+        const int to = begin + len / WAVES * (wave + 1) + len % WAVES * (wave + 1) / WAVES;
+        __syncthreads();  // tiles are there; the outputs before have been read
+        for (int i = lane; i < a.M * 4; i += 64)
+            reinterpret_cast<f32x4 *>(out)[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+        int it = a.by_down.of(from), is = from - it * stages;  // the tile and stage that are loaded next
+        u32x4 wr, hr, er, sr;
+        auto enter = [&] {
+            const unsigned v = __builtin_amdgcn_readfirstlane((int)tiles[it]);
+            const int e = (int)(v & 1023u), pairs = (int)(v >> 10 & 63u), first = (int)(v >> 16);
+            wr = rsrc_words(a.wd + e * a.down_bytes + (int64_t)n0 * KB, (unsigned)vn * (unsigned)KB);
+            hr = rsrc_words(a.h + (int64_t)first * a.I, (unsigned)pairs * XB);
+            er = rsrc_words(a.entries + first, (unsigned)pairs * 16u);
+            if constexpr (BLOCK)
+                sr = rsrc_words(a.sd + e * a.down_scales + (int64_t)(n0 / 128) * ib, (unsigned)ib * 4u);
+            else if constexpr (scaled_rows(TYPE))
+                sr = rsrc_words(a.sd + e * a.down_scales + n0, (unsigned)vn * 4u);
+        };
+        auto issue = [&](int slot) {
+            const unsigned k = (unsigned)is * 128u + piece;
+            const unsigned lds = lds0 + (unsigned)(slot * STAGE);
 #pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            const int r = BM <= 8 ? i16 % BM : j * 16 + i16;
-            read_x<TYPE, BM>(st + XAT, r, 0, g, bf[j]);
-            entry[j] = *reinterpret_cast<const u32x4 *>(st + EAT + r * 16);
-        }
-        if constexpr (BLOCK)
-            sc = *reinterpret_cast<const float *>(st + SAT);
-        else if constexpr (scaled_rows(TYPE))
-            rows = *reinterpret_cast<const f32x4 *>(st + SAT + (g * 4 % NB) * 4);
-        lds_read_wait();  // the stage is in registers: its slot may be written again
-        if (s + RING < to)
-            issue(slot);
-        slot = slot + 1 == RING ? 0 : slot + 1;
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            f32x4 p = BLOCK ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[j];
-#pragma unroll
-            for (int q = 0; q < 2 * PLANES; ++q)
-                p = mfma_bf16(af.v[q], bf[j][q], p);
-            if constexpr (BLOCK) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[j][e] = __builtin_fmaf(p[e], sc, acc[j][e]);
+            for (int c = 0; c < 2; ++c)
+                load_to_lds<true>(wr, k < (unsigned)KB ? (unsigned)(c * 8 + lrow) * (unsigned)KB + k : kOutOfRange,
+                                  lds + (unsigned)c * 1024u);
+            // rows beyond the tile's lie beyond the resource
+            if constexpr (BM == 4) {
+                const unsigned b = (unsigned)(is * PLANES + (PLANES == 2 ? lrow >> 2 : 0)) * 128u + piece;
+                if (PLANES == 2 || lane < 32)
+                    load_to_lds(hr, b < XB ? (unsigned)(lrow & 3) * XB + b : kOutOfRange, lds + XAT);
             } else {
-                acc[j] = p;
-            }
-        }
-        if (last) {
-            const int pairs = (int)(__builtin_amdgcn_readfirstlane((int)tiles[ct]) >> 10 & 63);
 #pragma unroll
-            for (int j = 0; j < TM; ++j) {
-                const int c = j * 16 + i16;
-                const bool live = c < pairs && (NB == 16 || g < 2);
-                const int token = (int)entry[j][0];
-                const unsigned weight = entry[j][1];  // a bit_cast of the element itself takes the first one
-                f32x4 v = acc[j] * __builtin_bit_cast(float, weight);
-                if constexpr (scaled_rows(TYPE))
-                    v *= rows;
-                f32x4 *at = reinterpret_cast<f32x4 *>(out + token * NB + g * 4);
-                // the pairs of an expert are in the order of their tokens: one that names it
-                // twice has two pairs side by side, which must not add at the same time
-                const int beside = __shfl_up(token, 1, 16);
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                if (!__ballot(live && i16 > 0 && token == beside)) {
-                    if (live)
-                        *at += v;
-                } else {
-                    for (int i = 0; i < 16; ++i) {
-                        if (live && i16 == i)
-                            *at += v;
-                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                    }
+                for (int h = 0; h < PLANES; ++h) {
+                    const unsigned b = (unsigned)(is * PLANES + h) * 128u + piece;
+#pragma unroll
+                    for (int c = 0; c < BM / 8; ++c)
+                        load_to_lds(hr, b < XB ? (unsigned)(c * 8 + lrow) * XB + b : kOutOfRange,
+                                    lds + XAT + (unsigned)(h * XPLANE + c * 1024));
                 }
             }
-            clear();
-        }
-        if (cs == stages) {
-            cs = 0;
-            ++ct;
-        }
-    }
+            if (lane < BM)  // lane i writes at lds + 16 i (4 i), the others nothing
+                load_to_lds(er, (unsigned)lane * 16u, lds + EAT);
+            if constexpr (TYPE != kWBf16)
+                if (lane < 16)
+                    load4_to_lds(sr, BLOCK ? (unsigned)is * 4u : (unsigned)lane * 4u, lds + SAT);
+            if (++is == stages) {
+                is = 0;
+                if (++it < nt)
+                    enter();
+            }
+        };
 
-    __syncthreads();
-    for (int o = threadIdx.x; o < a.M * NB / 4; o += WAVES * 64) {
-        const int m = o / (NB / 4), n = n0 + o % (NB / 4) * 4;
-        if (n >= a.H)
-            continue;
-        u32x2 r = {0, 0};  // H is a multiple of 8: all four are there
-        if (a.res)
-            r = *reinterpret_cast<const u32x2_any *>(a.res + m * a.ldr + n);
-        f32x4 z = widen4(r);
-        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        f32x4 acc[TM];
+        auto clear = [&] {
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w)
-            v += *reinterpret_cast<const f32x4 *>(outs + w * OUTS + o * 4);
-        if (a.res)
-            v += z;
-        *reinterpret_cast<u32x2_any *>(a.y + m * a.ldy + n) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            for (int i = 0; i < TM; ++i)
+                acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        };
+        clear();
+        int ct = it, cs = is;  // the tile and stage that are multiplied next
+        if (from < to) {
+            enter();
+#pragma unroll
+            for (int d = 0; d < RING; ++d)
+                if (from + d < to)
+                    issue(d);
+        }
+        int slot = 0;
+        for (int s = from; s < to; ++s) {
+            if (s + RING <= to)
+                stage_wait<(RING - 1) * LOADS>();
+            else
+                stage_wait<0>();
+            const uint8_t *st = ring + slot * STAGE;
+            Fragment<TYPE> af;
+            u32x4 bf[TM][2 * PLANES], entry[TM];
+            float sc = 1.0f;
+            f32x4 rows = {1.0f, 1.0f, 1.0f, 1.0f};
+            const bool last = ++cs == stages || s + 1 == to;
+            af.read(st + i16 * 128, g, i16 & 7);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int r = BM <= 8 ? i16 % BM : i * 16 + i16;
+                read_x<TYPE, BM>(st + XAT, r, 0, g, bf[i]);
+                entry[i] = *reinterpret_cast<const u32x4 *>(st + EAT + r * 16);
+            }
+            if constexpr (BLOCK)
+                sc = *reinterpret_cast<const float *>(st + SAT);
+            else if constexpr (scaled_rows(TYPE))
+                rows = *reinterpret_cast<const f32x4 *>(st + SAT + g * 16);
+            lds_read_wait();  // the stage is in registers: its slot may be written again
+            if (s + RING < to)
+                issue(slot);
+            slot = slot + 1 == RING ? 0 : slot + 1;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                f32x4 p = BLOCK ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[i];
+#pragma unroll
+                for (int q = 0; q < 2 * PLANES; ++q)
+                    p = mfma_bf16(af.v[q], bf[i][q], p);
+                if constexpr (BLOCK) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][e] = __builtin_fmaf(p[e], sc, acc[i][e]);
+                } else {
+                    acc[i] = p;
+                }
+            }
+            if (last) {
+                const int pairs = (int)(__builtin_amdgcn_readfirstlane((int)tiles[ct]) >> 10 & 63);
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const bool live = i * 16 + i16 < pairs;
+                    const int token = (int)entry[i][0];
+                    const unsigned weight = entry[i][1];  // a bit_cast of the element itself takes the first one
+                    f32x4 v = acc[i] * __builtin_bit_cast(float, weight);
+                    if constexpr (scaled_rows(TYPE))
+                        v *= rows;
+                    f32x4 *at = reinterpret_cast<f32x4 *>(out + token * 16 + g * 4);
+                    // the pairs of an expert are in the order of their tokens: one that names it
+                    // twice has two pairs side by side, which must not add at the same time
+                    const int beside = __shfl_up(token, 1, 16);
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    if (!__ballot(live && i16 > 0 && token == beside)) {
+                        if (live)
+                            *at += v;
+                    } else {
+                        for (int c = 0; c < 16; ++c) {
+                            if (live && i16 == c)
+                                *at += v;
+                            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                        }
+                    }
+                }
+                clear();
+            }
+            if (cs == stages) {
+                cs = 0;
+                ++ct;
+            }
+        }
+
+        __syncthreads();
+        auto sum = [&](int o) {
+            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < WAVES; ++k)
+                v += *reinterpret_cast<const f32x4 *>(outs + k * OUTS + o * 4);
+            return v;
+        };
+        if (len == T) {
+            for (int o = threadIdx.x; o < a.M * 4; o += WAVES * 64)
+                store(o, n0, sum(o));
+        } else {
+            // A block shares its first and its last 16 outputs at most. The parts go past the
+            // caches of the XCDs (agent scope), a block counts itself behind its stores, and the
+            // one that finds all others counted adds the parts up.
+            auto part = [&](int b) { return a.parts + (2 * b + ((int)a.begins[b][0] != j)) * (a.M * 16); };
+            float *mine = part(blockIdx.x);
+            for (int o = threadIdx.x; o < a.M * 4; o += WAVES * 64) {
+                const f32x4 v = sum(o);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    __hip_atomic_store(mine + o * 4 + e, v[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+            __builtin_amdgcn_s_waitcnt(kWaitStores);
+            __syncthreads();
+            // the blocks with the first and the last stage of these outputs
+            const int b0 = (int)share.of(j * T), b1 = (int)share.of(j * T + T - 1);
+            if (threadIdx.x == 0)
+                earlier = __hip_atomic_fetch_add(a.arrived + b0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            if (earlier == (unsigned)(b1 - b0))
+                for (int o = threadIdx.x; o < a.M * 4; o += WAVES * 64) {
+                    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int b = b0; b <= b1; ++b) {
+                        const float *p = part(b) + o * 4;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] += __hip_atomic_load(p + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    }
+                    store(o, n0, v);
+                }
+        }
     }
 }
 
@@ -841,8 +970,8 @@ namespace skg_host {
 namespace {
 
 // The kernels for one tile height: the first, for pairs of one wave or more, with x in LDS or
-// not (and the room that it takes), and the second, for 16 or 8 outputs a block, by the tokens
-// that it has room for: up to 16, 64 or 128.
+// not (and the room that it takes), and the second, by the tokens that it has room for: up to
+// 16, 64 or 128.
 struct UpKernel {
     const void *fn;
     int waves, room;
@@ -880,23 +1009,45 @@ UpKernel up_kernel(int64_t xbytes)
     return up_streamed<TYPE, BM, WAVE>();
 }
 
-template <int TYPE, int NB, int BM, int MC>
-const void *down_fn()
+struct DownKernel {
+    const void *fn;
+    int waves;
+};
+
+template <int TYPE, int BM, int MC>
+DownKernel down_of()
 {
-    constexpr int WAVES = 8;
-    constexpr int RING = ring_of(kLds - 4 * skg::kMostTiles - WAVES * MC * NB * 4, WAVES, skg::down_stage<TYPE, NB, BM>());
-    return (const void *)&skg::experts_down_kernel<TYPE, NB, BM, RING, WAVES, MC>;
+    constexpr int WAVES = MC == 128 || (BM == 32 && TYPE != skg::kWBf16) ? 4 : 8;
+    constexpr int RING = ring_of(kLds - 4 * skg::kMostTiles - 16 - WAVES * MC * 64, WAVES, skg::down_stage<TYPE, BM>());
+    return DownKernel{(const void *)&skg::experts_down_kernel<TYPE, BM, RING, WAVES, MC>, WAVES};
 }
 
 template <int TYPE, int BM>
-const void *down_kernel(int M, bool narrow)
+DownKernel down_kernel(int M)
 {
-    constexpr int B = BM == 32 ? 16 : BM;
-    if (M <= 16)  // tiles of 32 rows are for more
-        return narrow ? down_fn<TYPE, 8, B, 16>() : down_fn<TYPE, 16, B, 16>();
-    if (M <= 64)
-        return narrow ? down_fn<TYPE, 8, BM, 64>() : down_fn<TYPE, 16, BM, 64>();
-    return down_fn<TYPE, 8, BM, 128>();
+    // tiles of 32 rows are for more than 16 tokens
+    return M <= 16 ? down_of<TYPE, BM == 32 ? 16 : BM, 16>() : M <= 64 ? down_of<TYPE, BM, 64>() : down_of<TYPE, BM, 128>();
+}
+
+skg::Divisor divisor(unsigned d)
+{
+    unsigned shift = 0;
+    while ((UINT64_C(1) << shift) < d)
+        ++shift;
+    return skg::Divisor{(unsigned)((((UINT64_C(1) << shift) - d) << 32) / d + 1), shift};
+}
+
+// The element-wise kernels.
+template <int TYPE>
+int run_any(skg::ExpertArgs &a, hipStream_t stream)
+{
+    void *args[] = {&a};
+    const int64_t up = ((int64_t)a.M * a.k * a.I + 3) / 4, down = ((int64_t)a.M * a.H + 3) / 4, most = 1 << 20;
+    const int st = ops_launch((const void *)&skg::experts_up_any_kernel<TYPE>, dim3((unsigned)(up < most ? up : most)), 256,
+                              args, stream);
+    return st != SKINNY_OK ? st
+                           : ops_launch((const void *)&skg::experts_down_any_kernel<TYPE>,
+                                        dim3((unsigned)(down < most ? down : most)), 256, args, stream);
 }
 
 // Both kernels with tiles of BM rows.
@@ -909,30 +1060,29 @@ int run_rows(skg::ExpertArgs &a, int cus, hipStream_t stream)
     const int height = up.room ? BM : BM < 8 ? 8 : BM;
     int most = a.E + P / height;  // tiles, at most
     most = P < most ? P : most;
+    // the kernels count units and stages in 32 bits
+    const int64_t features = ((int64_t)a.I + 7) / 8, sets = ((int64_t)a.H + 15) / 16, per = skg::per_stage(TYPE);
+    const int64_t up_stages = (a.H + per - 1) / per, down_stages = (a.I + per - 1) / per;
+    if (most * features > INT32_MAX || features * up_stages > INT32_MAX || most * down_stages * sets > INT32_MAX)
+        return run_any<TYPE>(a, stream);
+    a.by_grid = divisor((unsigned)cus);
+    a.by_features = divisor((unsigned)features);
+    a.by_up = divisor((unsigned)up_stages);
+    a.by_down = divisor((unsigned)down_stages);
     void *args[] = {&a, &most};
     const int st = ops_launch(up.fn, dim3((unsigned)cus), up.waves * 64, args, stream);
     if (st != SKINNY_OK)
         return st;
-    const bool narrow = a.M > 64 || a.H < 16 * cus;
-    const void *down = height == BM ? down_kernel<TYPE, BM>(a.M, narrow) : down_kernel<TYPE, 8>(a.M, narrow);
-    const int nb = narrow ? 8 : 16;
-    return ops_launch(down, dim3((unsigned)(((int64_t)a.H + nb - 1) / nb)), 512, args, stream);
+    const DownKernel down = height == BM ? down_kernel<TYPE, BM>(a.M) : down_kernel<TYPE, 8>(a.M);
+    return ops_launch(down.fn, dim3((unsigned)kDownBlocks), down.waves * 64, args, stream);
 }
 
 template <int TYPE>
 int run_type(const skg::ExpertArgs &a, bool vector, int cus, hipStream_t stream)
 {
-    using namespace skg;
-    ExpertArgs args = a;
-    if (!vector) {
-        void *p[] = {&args};
-        const int64_t up = ((int64_t)a.M * a.k * a.I + 3) / 4, down = ((int64_t)a.M * a.H + 3) / 4;
-        const int st = ops_launch((const void *)&experts_up_any_kernel<TYPE>, dim3((unsigned)(up < (1 << 20) ? up : 1 << 20)),
-                                  256, p, stream);
-        return st != SKINNY_OK ? st
-                               : ops_launch((const void *)&experts_down_any_kernel<TYPE>,
-                                            dim3((unsigned)(down < (1 << 20) ? down : 1 << 20)), 256, p, stream);
-    }
+    skg::ExpertArgs args = a;
+    if (!vector)
+        return run_any<TYPE>(args, stream);
     const int P = a.M * a.k;
     // pairs of an expert that has any, were the pairs spread evenly
     const double some = a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, P)), even = P / some;
@@ -977,6 +1127,9 @@ int skinny_experts(const skinny_experts_t *e, hipStream_t stream)
     a.plan = reinterpret_cast<unsigned *>(ws);
     a.entries = reinterpret_cast<skg::u32x4 *>(ws + space.entries);
     a.h = reinterpret_cast<uint16_t *>(ws + space.h);
+    a.begins = reinterpret_cast<skg::u32x4 *>(ws + space.begins);
+    a.arrived = reinterpret_cast<unsigned *>(ws + space.arrived);
+    a.parts = reinterpret_cast<float *>(ws + space.parts);
     a.ldx = e->ldx;
     a.ldr = e->ldr;
     a.ldy = e->ldy;
@@ -989,6 +1142,7 @@ int skinny_experts(const skinny_experts_t *e, hipStream_t stream)
     a.H = e->H;
     a.I = e->I;
     a.act = e->act;
+    a.by_k = divisor((unsigned)e->k);
     const bool vector = experts_vector_ok(*e);
     for (int64_t m = 0; m < e->M; m += kExpertsRows) {
         a.M = (int)(e->M - m < kExpertsRows ? e->M - m : kExpertsRows);

@@ -56,22 +56,28 @@ inline int validate_route(const skinny_route_t *a)
 // Rows of one pair of launches: the pairs of that many rows are sorted at once.
 constexpr int32_t kExpertsRows = 128;
 
-// The workspace: the order of the pairs (for each a 16-byte entry, for each tile of them 4
-// bytes, 16 for their number) and then h.
+// Blocks of the second kernel.
+constexpr int32_t kDownBlocks = 256;
+
+// The workspace: the order of the pairs (16 bytes for the number of tiles, 4 for each, 16 for
+// each pair), h, and for each of the second kernel's blocks 16 bytes, a counter and two sets
+// of 16 outputs of every row.
 struct ExpertsSpace {
-    uint64_t tiles, entries, h, bytes;  // offsets, and all of it
+    uint64_t entries, h, begins, arrived, parts, bytes;  // offsets, and all of it
 };
 
 inline ExpertsSpace experts_space(int32_t M, int32_t k, int32_t E, int32_t I)
 {
-    const uint64_t pairs = (uint64_t)(M < kExpertsRows ? M : kExpertsRows) * (uint64_t)k;
+    const uint64_t rows = (uint64_t)(M < kExpertsRows ? M : kExpertsRows), pairs = rows * (uint64_t)k;
     // every expert may have a tile that is not full
     const uint64_t most = pairs < (uint64_t)E + pairs / 4 ? pairs : (uint64_t)E + pairs / 4;
     ExpertsSpace s{};
-    s.tiles = 16;
-    s.entries = s.tiles + (4 * most + 15) / 16 * 16;
+    s.entries = 16 + (4 * most + 15) / 16 * 16;
     s.h = s.entries + 16 * pairs;
-    s.bytes = s.h + (2 * pairs * (uint64_t)I + 15) / 16 * 16;
+    s.begins = s.h + (2 * pairs * (uint64_t)I + 15) / 16 * 16;
+    s.arrived = s.begins + 16 * (uint64_t)kDownBlocks;
+    s.parts = s.arrived + 4 * (uint64_t)kDownBlocks;
+    s.bytes = s.parts + 2 * (uint64_t)kDownBlocks * rows * 64;
     return s;
 }
 
