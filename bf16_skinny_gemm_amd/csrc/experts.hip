@@ -1086,7 +1086,16 @@ int run_type(const skg::ExpertArgs &a, bool vector, int cus, hipStream_t stream)
     const int P = a.M * a.k;
     // pairs of an expert that has any, were the pairs spread evenly
     const double some = a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, P)), even = P / some;
-    const int rows = even <= 2.0 ? 4 : even <= 7.0 ? 8 : even <= 12.0 || a.M <= 16 ? 16 : 32;
+    // A tile's rows of x (or h) cost LDS and loads whether there are pairs for them or not, and an
+    // expert with more pairs than rows is read again, from the caches at best. With narrow x,
+    // 16 rows of it stay in LDS. Both kernels, in microseconds, with 8 and with 16 rows:
+    // 61 tokens, 64 experts of 2048 x 1408, int8 (5.7 pairs each) 119 and 106; 32 tokens, 64 of
+    // 4096 x 1024, e4m3 (4.1) 135 and 149. With 16 and with 32: 100 tokens, 64 of 4096 x 1024,
+    // int8 (12.5) 221 and 267; 128 tokens, 8 of 4096 x 1536, int8 (32) 96 and 79, 8 of
+    // 2048 x 1024 (64) 59 and 62; 128 tokens, 64 of 4096 x 1024, bfloat16 (20) 539 and 365.
+    const bool bytes = TYPE != skg::kWBf16, narrow = a.H <= 2560;
+    const double eight = narrow ? 4.5 : 7.0, sixteen = bytes ? (narrow ? 64.0 : 20.0) : narrow ? 14.0 : 11.0;
+    const int rows = even <= 2.0 ? 4 : even <= eight ? 8 : even <= sixteen || a.M <= 16 ? 16 : 32;
     return rows == 4    ? run_rows<TYPE, 4>(args, cus, stream)
            : rows == 8  ? run_rows<TYPE, 8>(args, cus, stream)
            : rows == 16 ? run_rows<TYPE, 16>(args, cus, stream)
