@@ -1001,11 +1001,13 @@ UpKernel up_streamed()
 template <int TYPE, int BM, bool WAVE>
 UpKernel up_kernel(int64_t xbytes)
 {
-    static const UpKernel k[] = {up_resident<TYPE, BM, WAVE, 6>(), up_resident<TYPE, BM, WAVE, 4>(),
-                                 up_resident<TYPE, BM, WAVE, 3>()};
-    for (const UpKernel &u : k)
-        if ((xbytes + 255) / 256 * 256 * BM <= u.room)
-            return u;
+    if constexpr (BM < 32 || TYPE == skg::kWBf16 || !WAVE) {  // 8-bit weights, 32 rows and 64 pairs: x is wide
+        static const UpKernel k[] = {up_resident<TYPE, BM, WAVE, 6>(), up_resident<TYPE, BM, WAVE, 4>(),
+                                     up_resident<TYPE, BM, WAVE, 3>()};
+        for (const UpKernel &u : k)
+            if ((xbytes + 255) / 256 * 256 * BM <= u.room)
+                return u;
+    }
     return up_streamed<TYPE, BM, WAVE>();
 }
 

@@ -29,6 +29,12 @@ void add(std::set<uint64_t> &s, const void *p, int64_t rows, int64_t width, int6
             s.insert(b + (uint64_t)(r * stride + i));
 }
 
+bool within(const std::set<uint64_t> &a, uint64_t from, uint64_t bytes)
+{
+    const auto it = a.lower_bound(from);
+    return it != a.end() && *it < from + bytes;
+}
+
 bool meet(const std::set<uint64_t> &a, const std::set<uint64_t> &b)
 {
     for (uint64_t v : a)
@@ -109,7 +115,8 @@ int main()
             return fail("a router that overwrites an operand", i);
     }
     for (long i = 0; i < 100000; ++i) {
-        auto at = [&] { return 4096 + rng() % 1500 * 4; };
+        // the workspace, the largest by far, lies before, behind or among the others
+        auto at = [&] { return (1 << 20) + rng() % 1500 * 4; };
         skinny_experts_t a{};
         a.M = 1 + (int)(rng() % 3), a.E = 1 + (int)(rng() % 3), a.k = 1 + (int)(rng() % 2), a.H = 1 + (int)(rng() % 6);
         a.I = 1 + (int)(rng() % 6), a.type = (int)(rng() % 4);
@@ -117,7 +124,6 @@ int main()
         const int e = bytes ? 1 : 2, us = a.type == 2 ? 1 : a.I, ds = a.type == 2 ? 1 : a.H;
         a.x = ptr<void>(at()), a.ids = ptr<int32_t>(at()), a.weights = ptr<float>(at()), a.w_gate = ptr<void>(at());
         a.w_up = ptr<void>(at()), a.w_down = ptr<void>(at()), a.y = ptr<void>(at());
-        a.workspace = ptr<void>(at() & ~15ull);
         if (rng() & 1) {
             a.residual = rng() & 1 ? a.y : ptr<void>(at());
             a.ldr = a.H + (int)(rng() % 3);
@@ -129,12 +135,14 @@ int main()
             a.up_scale_stride = us + (int)(rng() % 3), a.down_scale_stride = ds + (int)(rng() % 3);
         }
         a.workspace_bytes = skg_host::experts_space(a.M, a.k, a.E, a.I).bytes;
+        const uint64_t to = at() & ~15ull;
+        a.workspace = ptr<void>(rng() & 1 ? to : (to - a.workspace_bytes) & ~15ull);
         if (validate_experts(&a) != SKINNY_OK)
             continue;
         ++checked;
-        std::set<uint64_t> y, ws, in, res;
+        std::set<uint64_t> y, in, res;
+        const uint64_t ws = reinterpret_cast<uintptr_t>(a.workspace), bytes_of = a.workspace_bytes;
         add(y, a.y, a.M, 2 * a.H, 2 * a.ldy);
-        add(ws, a.workspace, 1, (int64_t)a.workspace_bytes, 0);
         add(in, a.x, a.M, 2 * a.H, 2 * a.ldx);
         add(in, a.ids, 1, 4 * a.M * a.k, 0);
         add(in, a.weights, 1, 4 * a.M * a.k, 0);
@@ -148,7 +156,7 @@ int main()
         }
         add(res, a.residual, a.M, 2 * a.H, 2 * a.ldr);
         const bool same = a.residual == a.y && (a.ldr == a.ldy || a.M == 1);
-        if (meet(y, in) || meet(y, ws) || meet(ws, in) || meet(ws, res) || (meet(y, res) && !same))
+        if (meet(y, in) || within(y, ws, bytes_of) || within(in, ws, bytes_of) || within(res, ws, bytes_of) || (meet(y, res) && !same))
             return fail("experts that overwrite an operand", i);
     }
     std::printf("moe validation: ok (%ld extreme calls accepted, %ld small ones checked)\n", accepted, checked);

@@ -13,6 +13,7 @@ import math
 import pytest
 import torch
 
+from .int8_choices import CHOICES
 from .test_gpu_ops import (BF16, F32, LEAST, act_ref, bits, filled, gen, norm_ref, ops,  # noqa: F401
                            skg, walled, walls_hold)
 
@@ -257,6 +258,18 @@ def test_long_outputs(skg):  # noqa: F811
     for rows in (slice(0, 2), slice(M - 2, M)):
         ref = x[rows].double() @ w.double().t().contiguous()
         assert ((y[rows].double() - ref).abs() <= ref.abs() * BF16).all()
+
+
+@pytest.mark.parametrize("kernel", [(key, i) for key in CHOICES for i in range(len(CHOICES[key]))], ids=str)
+def test_kernel(skg, kernel):  # noqa: F811
+    (gated, _), i = kernel
+    M, N, K = CHOICES[kernel[0]][i]
+    if torch.cuda.get_device_properties(0).multi_processor_count != 256:
+        pytest.skip("the sizes are for 256 compute units")
+    for f32 in (False, True):
+        check_linear(skg, M, N, K, gated=bool(gated), act="silu" if gated else "gelu", bias=True, residual=not gated, f32=f32,
+                     ld=K + 16, ldy=N + 3, seed=N + i)
+    check_linear(skg, M, N, K, gated=bool(gated), seed=K + i)
 
 
 # ---- as they are used ----------------------------------------------------------

@@ -330,6 +330,39 @@ def test_experts_full_size(skg, kind):  # noqa: F811
         check_experts(skg, M, E, k, H, I, kind, seed=M)
 
 
+# For each height of tiles (4, 8, 16 and 32 rows) calls of one wave of pairs and of more, for up to
+# 16, 64 and 128 tokens, and widths whose rows of x leave LDS for 6, 4, 3 stages and none.
+TILES = {4: (((1, 64, 4), (40, 64, 1), (100, 300, 1), (30, 300, 4), (10, 200, 8)), (512, 9008, 12000, 14000)),
+         8: (((12, 16, 4), (50, 16, 1), (100, 32, 1), (16, 30, 6)), (520, 4000, 6000, 7200)),
+         16: (((16, 7, 4), (60, 6, 1), (120, 13, 1), (16, 14, 8)), (528, 2000, 2800, 4000)),
+         32: (((60, 2, 1), (100, 6, 2), (40, 2, 2)), (512, 1200, 1504, 2000)),
+         "32 of 8 bits": (((70, 1, 1), (64, 1, 2)), (512, 1200, 1504, 2000)),
+         "32 of 8 bits, wide": (((60, 2, 1), (100, 4, 1)), (2576,))}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", TILES)
+def test_experts_tiles(skg, rows, kind):  # noqa: F811
+    calls, widths = TILES[rows]
+    for M, E, k in calls:
+        ids = None
+        if k > E:  # the only expert, named twice
+            ids = torch.zeros(M, k, dtype=torch.int32, device="cuda")
+        for H in widths:
+            H = H // 16 * 16
+            check_experts(skg, M, E, k, H, 64, kind, ids=ids, residual=True, seed=H + M)
+            if H < 1000:
+                check_experts(skg, M, E, k, 80, H, kind, ids=ids, seed=H + M)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_experts_outputs_of_several_blocks(skg, kind):  # noqa: F811
+    """Sets of outputs that two and many blocks share, and blocks of several sets."""
+    for M, E, k, H, I in ((24, 40, 4, 16, 2048), (24, 40, 4, 64, 1024), (9, 12, 4, 1000 // 16 * 16, 640), (70, 30, 4, 144, 1280),
+                          (24, 24, 8, 4112, 256), (16, 16, 4, 8192, 128), (2, 8, 2, 5120, 2048)):
+        check_experts(skg, M, E, k, H, I, kind, residual=True, seed=H)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_experts_give_the_same_bits_and_rows_are_their_own(skg, kind):  # noqa: F811
     """NaN in one token stays there; the same call gives the same bits."""

@@ -7,6 +7,7 @@ import ctypes
 import pytest
 import torch
 
+from .int8_choices import CHOICES
 from .test_ops_abi import BAD, OK, R, RO, S, UNSUPPORTED, W, X, Y, needs_no_gpu, skg  # noqa: F401
 
 
@@ -100,6 +101,22 @@ def test_plan(skg):  # noqa: F811
     for kw in (dict(M=0), dict(N=0), dict(scales=2), dict(K=131072, ldx=131072)):
         with pytest.raises(skg.SkinnyError):
             plan(**kw)
+
+
+@pytest.mark.parametrize("key", CHOICES)
+def test_every_offered_kernel_is_chosen_at_some_size(skg, key):  # noqa: F811
+    gated, rows = key
+    def plan(M, N, K, f32):
+        return skg.skinny_linear_int8_default_plan(skg.LinearArgs(
+            x=1 << 40, W0=1 << 41, W1=1 << 42 if gated else None, y=1 << 43, x_scale=1 << 44, w0_scale=1 << 45,
+            w1_scale=1 << 46 if gated else None, ldx=K, ldy=N, M=M, N=N, K=K, scales=1, out_f32=f32))
+    plans = [plan(M, N, K, 0) for M, N, K in CHOICES[key]]
+    assert [p.index for p in plans] == list(range(plans[0].count))
+    for p, (M, N, K) in zip(plans, CHOICES[key]):
+        assert (M <= 8, M <= 16) == (rows == 0, rows <= 1)
+        assert plan(M, N, K, 1).as_dict() == p.as_dict()  # float32 outputs take the same
+        assert N > p.features and N % p.features and (M > p.rows or rows < 2) and M % p.rows
+        assert -(-K // 128) > (p.waves * p.ring if p.kind == skg.SKINNY_LINEAR_STREAM else 8) and K % 128
 
 
 def test_python_helpers_refuse(skg):  # noqa: F811
