@@ -232,6 +232,9 @@ _PY_KERNELS = {
         x, w, b, r, act, f32, x_scale=xs, w_scale=ws),
     "linear_gated_fp8": lambda x, xs, w, ws, u, us, b=None, bu=None, act="silu", f32=False: _linear_py(
         x, w, b, None, act, f32, u, bu, xs, ws, us),
+}
+# of the 8-bit integer operators, the router and the experts
+_PY_KERNELS_MORE = {
     "quantize_int8": _quantize_py,
     "rms_norm_int8": lambda x, w, eps: _norm_py(x, w, eps, None, "int8"),
     "add_rms_norm_int8": lambda x, r, w, eps: _norm_py(x, w, eps, r, "int8"),
@@ -300,7 +303,7 @@ for _schema in _SCHEMAS:
     _name = _schema.split("(")[0]
     if not CPP_OP:
         _LIB.define(_schema)
-        _LIB.impl(_name, _PY_KERNELS[_name], "CUDA")
+        _LIB.impl(_name, {**_PY_KERNELS, **_PY_KERNELS_MORE}[_name], "CUDA")
         _LIB.impl(_name, _refuse_cpu(_name), "CPU")
     torch.library.register_fake("skinny::" + _name, _FAKES[_name], lib=_LIB)
 rms_norm = torch.ops.skinny.rms_norm.default
