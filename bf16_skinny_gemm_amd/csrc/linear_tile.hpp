@@ -292,12 +292,19 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
                                          : u32x4{0, 0, 0, 0};
             }
         }
-    float xsv[TM];
+    float xsv[MODE == kInt8Row ? TM : 1];  // integer sums are multiplied when they become floats
     if constexpr (row_scaled(MODE)) {
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
             const int m = m0 + (wm * TM + j) * 16 + i16;
-            xsv[j] = m < a.M ? a.xs[m] : 0.0f;
+            const float xs = m < a.M ? a.xs[m] : 0.0f;
+            if constexpr (MODE == kInt8Row) {
+                xsv[j] = xs;
+            } else {
+#pragma unroll
+                for (int i = 0; i < TN; ++i)
+                    acc[i][j] *= xs;
+            }
         }
     }
     cols.settle();
@@ -312,7 +319,8 @@ __global__ __launch_bounds__(WN *WM * 64) void linear_tile_kernel(LinArgs a, int
                 constexpr int i = decltype(ic)::value;
                 const int p = ((i / TF) * NB + (wn * TF + i % TF) * 16) / 4 + g;
                 *reinterpret_cast<f32x4 *>(smem + row * (BN * 4) + (p ^ i16) * 16) =
-                    row_scaled(MODE) ? to_f32(acc[i][q * JP + j]) * xsv[q * JP + j] : to_f32(acc[i][q * JP + j]);
+                    MODE == kInt8Row ? to_f32(acc[i][q * JP + j]) * xsv[MODE == kInt8Row ? q * JP + j : 0]
+                                     : to_f32(acc[i][q * JP + j]);
             });
         });
         __syncthreads();
