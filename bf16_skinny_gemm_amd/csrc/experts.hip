@@ -19,7 +19,7 @@
 //    parts in the order of the blocks by the one that ends last: the same bits every time.
 //
 // 8-bit weights are widened to bfloat16 (exactly) and multiplied by x as it is, so that only
-// h and y are rounded: at 16 rows a tile, the matrix instructions cost nothing.
+// h and y are rounded.
 #include "ops_host.hpp"
 
 #include <cmath>
@@ -138,11 +138,17 @@ __device__ __forceinline__ void read_x(const uint8_t *at, int row, int plane, in
     }
 }
 
+// Tiles of up to 8 rows leave half of the instruction's 16 columns free. There h is held as two
+// bfloat16 values, the rounded one and what it leaves, in the columns 0..7 and 8..15: 16 bits of
+// it for no product more, where one rounding of it would be as large an error as that of y.
+constexpr bool split_h(int rows) { return rows <= 8; }
+constexpr int h_rows(int rows) { return split_h(rows) ? 2 * rows : rows; }
+
 // Bytes of a stage: weights, x or h, and what belongs to them.
 template <int TYPE, int BM, bool RESIDENT>
 constexpr int up_stage() { return 2048 + (RESIDENT ? 0 : planes<TYPE>() * BM * 128) + (TYPE == kWBf16 ? 0 : 64); }
 template <int TYPE, int BM>
-constexpr int down_stage() { return 2048 + planes<TYPE>() * BM * 128 + BM * 16 + (TYPE == kWBf16 ? 0 : 64); }
+constexpr int down_stage() { return 2048 + planes<TYPE>() * h_rows(BM) * 128 + BM * 16 + (TYPE == kWBf16 ? 0 : 64); }
 
 // ---- the pairs by expert -----------------------------------------------------------
 
@@ -505,8 +511,16 @@ __global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
                 const int r = j * 16 + i16;
                 if (lane < 32 && r < pairs && f < a.I) {  // I is a multiple of 8: all four are there
                     z = activate4(z, a.act) * o;
-                    *reinterpret_cast<u32x2 *>(a.h + (int64_t)(first + r) * a.I + f) =
-                        u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+                    const u32x2 hi = {pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+                    uint16_t *at = a.h + (int64_t)(first + r) * a.I * (split_h(BM) ? 2 : 1) + f;
+                    *reinterpret_cast<u32x2 *>(at) = hi;
+                    if constexpr (split_h(BM)) {
+                        const f32x4 w = widen4(hi);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)  // of an infinity nothing is left
+                            z[e] = __builtin_fabsf(w[e]) == __builtin_inff() ? 0.0f : z[e] - w[e];
+                        *reinterpret_cast<u32x2 *>(at + a.I) = u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
+                    }
                 }
             }
         };
@@ -622,9 +636,11 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
     constexpr bool BLOCK = TYPE == kWBlock;
     constexpr int PLANES = planes<TYPE>();
     constexpr int TM = (BM + 15) / 16;
-    constexpr int XAT = 2048, XPLANE = BM * 128, EAT = XAT + PLANES * XPLANE, SAT = EAT + BM * 16;
+    constexpr bool SPLIT = split_h(BM);
+    constexpr int HR = h_rows(BM);  // rows of h in LDS: split, those of the first values, then the others
+    constexpr int XAT = 2048, XPLANE = HR * 128, EAT = XAT + PLANES * XPLANE, SAT = EAT + BM * 16;
     constexpr int STAGE = down_stage<TYPE, BM>();
-    constexpr int HLOADS = BM == 4 ? 1 : PLANES * BM / 8;  // 8 rows each: with 4 rows both planes at once
+    constexpr int HLOADS = PLANES * HR / 8;  // 8 rows each
     constexpr int LOADS = 2 + HLOADS + 1 + (TYPE == kWBf16 ? 0 : 1);
     constexpr int OUTS = MC * 16;  // floats of a wave
     static_assert((BM == 4 || BM % 8 == 0) && BM <= 32 && (RING - 1) * LOADS < 64, "tile");
@@ -692,7 +708,7 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
             const unsigned v = __builtin_amdgcn_readfirstlane((int)tiles[it]);
             const int e = (int)(v & 1023u), pairs = (int)(v >> 10 & 63u), first = (int)(v >> 16);
             wr = rsrc_words(a.wd + e * a.down_bytes + (int64_t)n0 * KB, (unsigned)vn * (unsigned)KB);
-            hr = rsrc_words(a.h + (int64_t)first * a.I, (unsigned)pairs * XB);
+            hr = rsrc_words(a.h + (int64_t)first * a.I * (SPLIT ? 2 : 1), (unsigned)pairs * XB * (SPLIT ? 2 : 1));
             er = rsrc_words(a.entries + first, (unsigned)pairs * 16u);
             if constexpr (BLOCK)
                 sr = rsrc_words(a.sd + e * a.down_scales + (int64_t)(n0 / 128) * ib, (unsigned)ib * 4u);
@@ -707,18 +723,14 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
                 load_to_lds<true>(wr, k < (unsigned)KB ? (unsigned)(c * 8 + lrow) * (unsigned)KB + k : kOutOfRange,
                                   lds + (unsigned)c * 1024u);
             // rows beyond the tile's lie beyond the resource
-            if constexpr (BM == 4) {
-                const unsigned b = (unsigned)(is * PLANES + (PLANES == 2 ? lrow >> 2 : 0)) * 128u + piece;
-                if (PLANES == 2 || lane < 32)
-                    load_to_lds(hr, b < XB ? (unsigned)(lrow & 3) * XB + b : kOutOfRange, lds + XAT);
-            } else {
 #pragma unroll
-                for (int h = 0; h < PLANES; ++h) {
-                    const unsigned b = (unsigned)(is * PLANES + h) * 128u + piece;
+            for (int h = 0; h < PLANES; ++h) {
+                const unsigned b = (unsigned)(is * PLANES + h) * 128u + piece;
 #pragma unroll
-                    for (int c = 0; c < BM / 8; ++c)
-                        load_to_lds(hr, b < XB ? (unsigned)(c * 8 + lrow) * XB + b : kOutOfRange,
-                                    lds + XAT + (unsigned)(h * XPLANE + c * 1024));
+                for (int c = 0; c < HR / 8; ++c) {
+                    const int r = c * 8 + lrow;  // of LDS
+                    const unsigned row = SPLIT ? (unsigned)(r % BM * 2 + r / BM) : (unsigned)r;
+                    load_to_lds(hr, b < XB ? row * XB + b : kOutOfRange, lds + XAT + (unsigned)(h * XPLANE + c * 1024));
                 }
             }
             if (lane < BM)  // lane i writes at lds + 16 i (4 i), the others nothing
@@ -763,8 +775,8 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
             af.read(st + i16 * 128, g, i16 & 7);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
-                const int r = BM <= 8 ? i16 % BM : i * 16 + i16;
-                read_x<TYPE, BM>(st + XAT, r, 0, g, bf[i]);
+                const int r = SPLIT ? i16 % BM : i * 16 + i16;
+                read_x<TYPE, HR>(st + XAT, SPLIT ? r + i16 / 8 * BM : r, 0, g, bf[i]);
                 entry[i] = *reinterpret_cast<const u32x4 *>(st + EAT + r * 16);
             }
             if constexpr (BLOCK)
@@ -793,6 +805,10 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
                 const int pairs = (int)(__builtin_amdgcn_readfirstlane((int)tiles[ct]) >> 10 & 63);
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
+                    if constexpr (SPLIT)  // both parts of h, in the columns up to 7
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[i][e] += __shfl_xor(acc[i][e], 8, 64);
                     const bool live = i * 16 + i16 < pairs;
                     const int token = (int)entry[i][0];
                     const unsigned weight = entry[i][1];  // a bit_cast of the element itself takes the first one
@@ -890,7 +906,7 @@ __device__ __forceinline__ float any_sum(float v)
     return v;
 }
 
-// One wave per pair and feature: h of pair p is row p.
+// One wave per pair and feature: h of pair p is row p, in float32.
 template <int TYPE>
 __global__ __launch_bounds__(256) void experts_up_any_kernel(ExpertArgs a)
 {
@@ -923,7 +939,7 @@ __global__ __launch_bounds__(256) void experts_up_any_kernel(ExpertArgs a)
         float z[1] = {v[0]};
         activate(z, a.act);
         if (lane == 0)
-            a.h[o] = f32_to_bf16(z[0] * v[1]);
+            reinterpret_cast<float *>(a.h)[o] = z[0] * v[1];
     }
 }
 
@@ -945,7 +961,7 @@ __global__ __launch_bounds__(256) void experts_down_any_kernel(ExpertArgs a)
             const float *s = TYPE == kWBf16 ? nullptr : a.sd + e * a.down_scales;
             float sum = 0.0f;
             for (int i = lane; i < a.I; i += 64) {
-                const float t = bf16_to_f32(a.h[(int64_t)p * a.I + i]) * weight_at<TYPE>(w, (int64_t)n * a.I + i);
+                const float t = reinterpret_cast<const float *>(a.h)[(int64_t)p * a.I + i] * weight_at<TYPE>(w, (int64_t)n * a.I + i);
                 if constexpr (TYPE == kWBlock)
                     sum = __builtin_fmaf(t, s[(int64_t)(n >> 7) * ib + (i >> 7)], sum);
                 else

@@ -60,7 +60,7 @@ constexpr int32_t kExpertsRows = 128;
 constexpr int32_t kDownBlocks = 256;
 
 // The workspace: the order of the pairs (16 bytes for the number of tiles, 4 for each, 16 for
-// each pair), h, and for each of the second kernel's blocks 16 bytes, a counter and two sets
+// each pair), h in up to 4 bytes a value, and for each of the second kernel's blocks 16 bytes, a counter and two sets
 // of 16 outputs of every row.
 struct ExpertsSpace {
     uint64_t entries, h, begins, arrived, parts, bytes;  // offsets, and all of it
@@ -74,7 +74,7 @@ inline ExpertsSpace experts_space(int32_t M, int32_t k, int32_t E, int32_t I)
     ExpertsSpace s{};
     s.entries = 16 + (4 * most + 15) / 16 * 16;
     s.h = s.entries + 16 * pairs;
-    s.begins = s.h + (2 * pairs * (uint64_t)I + 15) / 16 * 16;
+    s.begins = s.h + (4 * pairs * (uint64_t)I + 15) / 16 * 16;
     s.arrived = s.begins + 16 * (uint64_t)kDownBlocks;
     s.parts = s.arrived + 4 * (uint64_t)kDownBlocks;
     s.bytes = s.parts + 2 * (uint64_t)kDownBlocks * rows * 64;

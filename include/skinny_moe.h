@@ -62,12 +62,14 @@ int skinny_route(const skinny_route_t *args, hipStream_t stream);
  * are bfloat16; y may be the residual itself (same pointer and stride), no other overlap of
  * y or the workspace with another operand is accepted.
  * Weights are bfloat16, or 8-bit (e4m3 or integers) with float32 scales, each times x as it
- * is: 8-bit values are bfloat16 ones, exactly. Sums are held in float32; h is
- * rounded to bfloat16 between the projections, as skinny_linear_bf16 stores it, and y once.
+ * is: 8-bit values are bfloat16 ones, exactly. Sums are held in float32 and y is rounded once.
+ * Between the projections h is held as two bfloat16 values (16 bits) where experts are read for
+ * 4 or 8 rows, and rounded to one, as skinny_linear_bf16 stores it, where for more.
  * Two kernels for every 128 rows, with h and the order of the pairs (m, j) by expert in the
- * workspace; each expert that a row names is read once, except that one with many rows is
- * read again every 32 (through the caches). For up to some hundred rows; a prompt of
- * thousands reads every expert again for each 128 of them.
+ * workspace; each expert that a row names is read once for every 4 to 32 of its rows (how many
+ * goes by the rows that an expert has on average), most of them from the caches after the first
+ * time. For up to some hundred rows; a prompt of thousands reads every expert again for each
+ * 128 of them.
  * Fast path: x, ldx, weights and their strides multiples of 16 bytes, H and I multiples of 8
  * (bfloat16) or 16. Others run an element-wise kernel, which is right and slow.
  * 1 <= E <= 1024, 1 <= k <= 32; H, I >= 1.

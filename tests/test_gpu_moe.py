@@ -191,7 +191,7 @@ def make_weight(g, E, N, K, kind, pad):
 
 
 def check_experts(skg, M, E, k, H, I, kind, *, act="silu", residual=False, ids=None, ldx=None, ldy=None, pad=0, shift=0,  # noqa: F811
-                  seed=0, in_place=False, merged=False):
+                  seed=0, in_place=False, merged=False, h_rounding=BF16):
     g = gen(seed)
     x = torch.randn(M, H, generator=g, device="cuda").to(torch.bfloat16)
     gate, gs, gw = make_weight(g, E, I, H, kind, pad)
@@ -238,7 +238,7 @@ def check_experts(skg, M, E, k, H, I, kind, *, act="silu", residual=False, ids=N
         ea = ea + (32 * F32 * z.abs() if act in ("silu", "gelu_tanh") else 0)
         h = a * u
         eh = ea * u.abs() + (a.abs() + ea) * eu
-        eh = eh + (h.abs() + eh) * (BF16 + 4 * F32)
+        eh = eh + (h.abs() + eh) * (h_rounding + 4 * F32)
         w = weights[m, j].double()[:, None]
         ref.index_add_(0, m, w * (h @ dw[e].t().contiguous()))
         down_abs = dw[e].abs().t().contiguous()
@@ -353,6 +353,34 @@ def test_experts_tiles(skg, rows, kind):  # noqa: F811
             check_experts(skg, M, E, k, H, 64, kind, ids=ids, residual=True, seed=H + M)
             if H < 1000:
                 check_experts(skg, M, E, k, 80, H, kind, ids=ids, seed=H + M)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", (4, 8))
+def test_experts_of_few_rows_hold_h_in_two_parts(skg, rows, kind):  # noqa: F811
+    """A bfloat16 value and what it leaves, rounded to bfloat16: off by 2^-16 of h at most."""
+    for M, E, k in TILES[rows][0][:4]:
+        check_experts(skg, M, E, k, 256, 144, kind, seed=M, h_rounding=BF16 ** 2)
+    check_experts(skg, 3, 8, 2, 249, 135, kind, seed=9, h_rounding=BF16 ** 2)  # element by element: in float32
+
+
+@pytest.mark.parametrize("M,E,H", [(2, 16, 64), (12, 16, 64), (40, 2, 64), (2, 16, 60)])
+def test_experts_of_infinite_h(skg, M, E, H):  # noqa: F811
+    """An infinite h makes its outputs infinite, not NaN, also where h is held in two parts."""
+    I = 32
+    x = torch.full((M, H), 2.0 ** 63, device="cuda").to(torch.bfloat16)
+    gate, up = torch.zeros(E, I, H, device="cuda"), torch.zeros(E, I, H, device="cuda")
+    gate[:, :, 0], up[:, :, 0] = 1.0, 2.0        # 2^63, 2^64: h is 2^127
+    gate[:, 3, 0], up[:, 3, 0] = 1.5, 2.0 ** 30  # overflows
+    down = torch.full((E, H, I), 1.0, device="cuda")
+    down[:, 1] = -1.0
+    down[:, 2:, 3] = 0.0
+    down[:, 2:] *= 2.0 ** -10
+    ids = torch.arange(M, device="cuda").remainder(E).to(torch.int32)[:, None]
+    w = [v.to(torch.bfloat16) for v in (gate, up, down)]
+    y = skg.experts(x, ids, torch.ones(M, 1, device="cuda"), *w, act="none").float()
+    assert (y[:, 0] == math.inf).all() and (y[:, 1] == -math.inf).all()
+    assert y[:, 2:].isnan().all()  # infinity times zero
 
 
 @pytest.mark.parametrize("kind", KINDS)

@@ -96,7 +96,7 @@ def test_workspace_bytes(skg):  # noqa: F811
     assert f(0, 2, 8, 128) == f(4, 0, 8, 128) == f(4, 33, 8, 128) == f(4, 2, 0, 128) == f(4, 2, 8, 0) == f(-1, 2, 8, 128) == 0
     assert f(1, 1, 1, 1) >= 2 and f(4, 2, 8, 128) >= 4 * 2 * 128 * 2
     # one pass at a time: h, two sets of 16 outputs for 256 blocks and every row, and little more
-    assert f(128, 8, 288, 1024) == f(10 ** 6, 8, 288, 1024) < 128 * 8 * 1024 * 2 + 2 * 256 * 128 * 64 + (1 << 16)
+    assert f(128, 8, 288, 1024) == f(10 ** 6, 8, 288, 1024) < 128 * 8 * 1024 * 4 + 2 * 256 * 128 * 64 + (1 << 16)
     sizes = [f(m, 4, 64, 96) for m in range(1, 200)]
     assert sizes == sorted(sizes)
     need = f(4, 2, 8, 128)
