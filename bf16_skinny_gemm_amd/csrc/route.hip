@@ -224,7 +224,12 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a)
     float w = 0.0f;
     if (lane < a.k) {
         const float l = logits[mine];
-        w = SOFTMAX ? expf(l - top) : 1.0f / (1.0f + expf(-l));
+        if constexpr (SOFTMAX) {
+            w = expf(l - top);
+        } else {
+            const float t = expf(-__builtin_fabsf(l));  // the other way round, exp(-l) overflows below -88
+            w = (l < 0.0f ? t : 1.0f) / (1.0f + t);
+        }
     }
     if (a.renormalize) {
         const float all = wave_add(w);

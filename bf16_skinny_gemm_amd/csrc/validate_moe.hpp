@@ -59,9 +59,9 @@ constexpr int32_t kExpertsRows = 128;
 // Blocks of the second kernel.
 constexpr int32_t kDownBlocks = 256;
 
-// The workspace: the order of the pairs (16 bytes for the number of tiles, 4 for each, 16 for
-// each pair), h in up to 4 bytes a value, and for each of the second kernel's blocks 16 bytes, a counter and two sets
-// of 16 outputs of every row.
+// The workspace: the order of the pairs (16 bytes for the number of tiles and the second kernel's
+// runs, 4 for each tile, 16 for each pair), h in up to 4 bytes a value, and for each of the second
+// kernel's blocks 16 bytes, a counter and two sets of 16 outputs of every row.
 struct ExpertsSpace {
     uint64_t entries, h, begins, arrived, parts, bytes;  // offsets, and all of it
 };
@@ -140,7 +140,8 @@ inline int validate_experts(const skinny_experts_t *a)
 }
 
 // x, the weights and h can be read in 16-byte pieces, and the 32-bit byte offsets of the
-// kernels' buffer resources reach: 128 rows of x, 32 of h, 16 of a weight.
+// kernels' buffer resources reach: 128 rows of x, 32 of h (16 where it has two parts), 16 of a
+// weight.
 inline bool experts_vector_ok(const skinny_experts_t &a)
 {
     const int64_t piece = a.type == SKINNY_WEIGHTS_BF16 ? 8 : 16;

@@ -138,6 +138,15 @@ def test_route_special_rows(skg):  # noqa: F811
     check_route(skg, x[:1, :64].contiguous(), 64, "sigmoid", bias[:64].contiguous())
 
 
+def test_route_small_sigmoids(skg):  # noqa: F811
+    """Scores below the normal float32 values keep what bits they have: here 2^-149 / exp(-95) of
+    them, which is 2^-12, half of it for each of two scores and twice as much for their sum."""
+    logits = -95.0 + torch.rand(9, 70, generator=gen(4), device="cuda")
+    ids, w = skg.route(logits, 6, "sigmoid")
+    want, wref = route_ref(logits, 6, "sigmoid", None, 1, 1, True, 1.0)
+    assert torch.equal(ids.cpu(), want) and ((w.double().cpu() - wref).abs() <= 2.0 ** -11 * wref).all()
+
+
 def test_route_strides_and_shapes(skg, ops):  # noqa: F811
     flat, view = walled(7, 96, 131, torch.float32)
     view.copy_(torch.randn(7, 96, generator=gen(1), device="cuda"))
