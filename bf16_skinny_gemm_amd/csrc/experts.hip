@@ -20,6 +20,15 @@
 //
 // 8-bit weights are widened to bfloat16 (exactly) and multiplied by x as it is, so that only
 // h and y are rounded.
+//
+// What it measured, cold weights, both kernels by the trace (least of 36): one token, 8 experts of
+// 4096 x 1024 in bfloat16 22.9 + 13.1 us (5.6 TB/s); 5 tokens, 8 of 288 experts of that size
+// with block scales 52.4 + 27.8 (5.9); 61 tokens, 6 of 64 of 2048 x 1408 in int8 61.6 + 44.5
+// (5.2); 37 tokens, 2 of 16 of 4096 x 1536 in bfloat16 61.2 + 38.3 (6.0). So HBM bounds them.
+// Three tokens, 4 of 64 of 2048 x 768 with row scales take 12.4 + 10.4 (2.3 TB/s): an empty
+// launch of the first kernel, with its plan, is 2.2 to 4 us and of the second 4, and each wave
+// has 9 stages, fewer than two rings. Equal runs cost the largest calls of few tokens 3% against
+// blocks that the hardware hands out, and gain all others up to half.
 #include "ops_host.hpp"
 
 #include <cmath>
@@ -140,7 +149,11 @@ __device__ __forceinline__ void read_x(const uint8_t *at, int row, int plane, in
 
 // Tiles of up to 8 rows leave half of the instruction's 16 columns free. There h is held as two
 // bfloat16 values, the rounded one and what it leaves, in the columns 0..7 and 8..15: 16 bits of
-// it for no product more, where one rounding of it would be as large an error as that of y.
+// it for no product more, where one rounding of it would be as large an error as that of y. It
+// costs nothing with 4 rows, and 6 us of 96 with 8 (37 tokens, 16 experts of 4096 x 1536,
+// bfloat16), where a compute unit takes in as much of h as of the weights. Tiles of more rows
+// hold h in one bfloat16 value, as a projection of its own would store it: two would double
+// the products and loads, and the many pairs average the error of each out.
 constexpr bool split_h(int rows) { return rows <= 8; }
 constexpr int h_rows(int rows) { return split_h(rows) ? 2 * rows : rows; }
 
@@ -1107,8 +1120,9 @@ int run_type(const skg::ExpertArgs &a, bool vector, int cus, hipStream_t stream)
     // A tile's rows of x (or h) cost LDS and loads whether there are pairs for them or not, and an
     // expert with more pairs than rows is read again, from the caches at best. With narrow x,
     // 16 rows of it stay in LDS. Both kernels, in microseconds, with 8 and with 16 rows:
-    // 61 tokens, 64 experts of 2048 x 1408, int8 (5.7 pairs each) 119 and 106; 32 tokens, 64 of
-    // 4096 x 1024, e4m3 (4.1) 135 and 149. With 16 and with 32: 100 tokens, 64 of 4096 x 1024,
+    // 61 tokens, 64 experts of 2048 x 1408, int8 (5.7 pairs each) 129 and 107; 32 tokens, 64 of
+    // 4096 x 1024, e4m3 (2.4) 116 and 124, with 4 rows 121, and (4.1) 147 and 150, with 4 rows 185.
+    // With 16 and with 32: 100 tokens, 64 of 4096 x 1024,
     // int8 (12.5) 221 and 267; 128 tokens, 8 of 4096 x 1536, int8 (32) 96 and 79, 8 of
     // 2048 x 1024 (64) 59 and 62; 128 tokens, 64 of 4096 x 1024, bfloat16 (20) 539 and 365.
     const bool bytes = TYPE != skg::kWBf16, narrow = a.H <= 2560;

@@ -11,7 +11,9 @@
 // as the operand registers of the matrix instructions want them. Bound by HBM (few rows,
 // medians of cold launches: 1 x 4096 x 4096 bfloat16 6.2 us, 5.5 TB/s; 1 x 12576 x 4096 e4m3
 // 9.1 us, 5.6 TB/s) or by the 64 bytes a clock of W and x (many: 100 x 4096 x 8192 e4m3
-// 13.5 us, 58 KB/us a compute unit over the whole launch).
+// 13.5 us, 58 KB/us a compute unit over the whole launch). 8-bit integers go the same way, as
+// integers: 1 x 12576 x 4096 8.2 to 10.4 us (6.2 TB/s at best), 5 x 77440 x 4096 45.9 (6.9),
+// 100 x 4096 x 8192 12.0.
 #pragma once
 
 #include "lds_load.hpp"
