@@ -106,8 +106,21 @@ __device__ __forceinline__ unsigned pack_e4m3(float a, float b, float c, float d
 }
 
 // The same to 8-bit integers, nearest-even: |y / scale| <= 127 (1 + 2^-22), which rounds to
-// 127. NaN gives 0, beside a scale of NaN.
+// 127. NaN gives 0, beside a scale of NaN. Half of the largest
+// value is 63.5 steps, and the product with the reciprocal alone lies on another side of the tie
+// than the quotient for some mantissas; so here the product is corrected by what it leaves of y:
+// the correctly rounded quotient, but where that lies within 2^-22 of its last bit from a tie of
+// its own, which no bfloat16 y does. 8192 x 4096 rows 19.1 us, with divisions 23.8, by the
+// reciprocal alone 18.6. Beside an infinite scale it is NaN, which gives 0 too.
 __device__ __forceinline__ unsigned to_int8(float v) { return (unsigned)(int)__builtin_rintf(v) & 0xFFu; }
+
+// y in steps of its scale, of which g is the reciprocal.
+template <int OUT>
+__device__ __forceinline__ float in_steps(float y, float scale, float g)
+{
+    const float q = y * g;
+    return int8_out(OUT) ? __builtin_fmaf(__builtin_fmaf(-q, scale, y), g, q) : q;
+}
 
 template <int OUT>
 __device__ __forceinline__ unsigned pack_bytes(float a, float b, float c, float d)
@@ -303,8 +316,10 @@ __global__ __launch_bounds__(WPR >= 4 ? WPR * 64 : 256) void norm_kernel(NormArg
                     a.scale[rr * a.groups + (c >> 7)] = sc;
             }
             u32x2 o;
-            o[0] = pack_bytes<OUT>(hw[p][0] * f * g, hw[p][1] * f * g, hw[p][2] * f * g, hw[p][3] * f * g);
-            o[1] = pack_bytes<OUT>(hw[p][4] * f * g, hw[p][5] * f * g, hw[p][6] * f * g, hw[p][7] * f * g);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                o[q] = pack_bytes<OUT>(in_steps<OUT>(hw[p][4 * q] * f, sc, g), in_steps<OUT>(hw[p][4 * q + 1] * f, sc, g),
+                                       in_steps<OUT>(hw[p][4 * q + 2] * f, sc, g), in_steps<OUT>(hw[p][4 * q + 3] * f, sc, g));
             if (c < a.D)
                 store8<NT>(y + c, o, a.D - c);
         }
@@ -368,7 +383,7 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a)
             for (int64_t i = t; i < a.D; i += 256) {
                 const float h = h_at((int)i);
                 store_h((int)i, h);
-                y[i] = (uint8_t)pack_bytes<OUT>(weighted(h, (int)i) * f * g, 0.0f, 0.0f, 0.0f);
+                y[i] = (uint8_t)pack_bytes<OUT>(in_steps<OUT>(weighted(h, (int)i) * f, sc, g), 0.0f, 0.0f, 0.0f);
             }
         } else {
             // a wave takes a group of 128 columns, two per lane

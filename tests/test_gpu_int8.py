@@ -126,6 +126,45 @@ def test_in_place(skg):  # noqa: F811
         assert torch.equal(q, q0) and torch.equal(s, s0) and torch.equal(bits(h), bits(h0))
 
 
+def rows_of_every_value():
+    """For each bfloat16 mantissa of the largest value a row of all the smaller ones of eight
+    exponents, both signs: half of the largest is 63.5 steps, up to the scale's rounding."""
+    m = torch.arange(128, 256, dtype=torch.float64)
+    v = (m[:, None] * 2.0 ** -torch.arange(8)).flatten()
+    v = torch.cat([v, -v]).expand(128, -1)
+    return torch.where(v.abs() <= m[:, None], v, 0.0 * v).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("D", (2048, 33000))
+@pytest.mark.parametrize("power", (-107, -60, 0, 40, 120))
+def test_rows_are_divided_by_their_scale(skg, power, D):  # noqa: F811
+    """The quotient is float32's own, so that values half way between two integers go where a
+    division puts them; no tolerance."""
+    x = torch.zeros(128, D, dtype=torch.bfloat16)
+    x[:, :2048] = rows_of_every_value() * 2.0 ** power
+    q, scale = (t.cpu() for t in skg.quantize_int8(x.cuda()))
+    assert torch.equal(scale, x.float().abs().amax(dim=1) / TOP)
+    want = torch.round(x.float() / scale[:, None]).to(torch.int8)
+    assert torch.equal(q, want), (int((q != want).sum()), (q != want).nonzero()[:4].tolist())
+
+
+@pytest.mark.parametrize("D", (2048, 33000))
+@pytest.mark.parametrize("residual", (False, True))
+def test_norms_are_divided_by_their_scale(skg, residual, D):  # noqa: F811
+    """The same of a norm: h is 1 or -1, so that its factor is 1 and y the weight's value."""
+    x = torch.ones(3, D, dtype=torch.bfloat16, device="cuda")
+    x[1] = -1.0
+    x[2, ::2] = -1.0
+    h = x.float().cpu()
+    r = x * 0.5 if residual else None
+    w = torch.zeros(128, D, dtype=torch.bfloat16)
+    w[:, :2048] = rows_of_every_value()
+    for row in w:
+        q, scale = (t.cpu() for t in skg.rms_norm(x - r if residual else x, row.cuda(), 0.0, residual=r, quant="int8")[:2])
+        assert torch.equal(scale, (row.float().abs().max() / TOP).expand(3))
+        assert torch.equal(q, torch.round(row.float() * h / scale[:, None]).to(torch.int8))
+
+
 # ---- projections -------------------------------------------------------------
 
 def check_linear(skg, M, N, K, *, gated=False, act="none", bias=False, residual=False, f32=False, ld=None,  # noqa: F811
