@@ -47,6 +47,11 @@ __device__ __forceinline__ unsigned long long order_of(double v)
     return v != v ? ~0ull : b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
+__device__ __forceinline__ float value_of(unsigned o)
+{
+    return __builtin_bit_cast(float, o >> 31 ? o & 0x7FFFFFFFu : ~o);
+}
+
 __device__ __forceinline__ double value_of(unsigned long long o)
 {
     return __builtin_bit_cast(double, o >> 63 ? o & 0x7FFFFFFFFFFFFFFFull : ~o);
@@ -233,14 +238,24 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a)
             key[v] = e0 + v == e ? 0 : key[v];
     }
 
+    const float l = lane < a.k ? logits[mine] : 0.0f;
+    if (a.renormalize) {
+        // The chosen may all lie far below the row's largest (with a bias, or as sigmoids), where
+        // float32 holds little or nothing of their scores: what these have in common, the
+        // exponential of the largest chosen logit, leaves the quotients first. Below exp(-745),
+        // the least of float64, scores are 0: masks of the lowest finite value leave nothing,
+        // as those of -infinity.
+        const float most = value_of(wave_max(lane < a.k ? order_of(l) : 0u)), below = SOFTMAX ? most - top : most;
+        if (below >= -745.0f && below <= 0.0f)
+            top = most;
+    }
     float w = 0.0f;
     if (lane < a.k) {
-        const float l = logits[mine];
         if constexpr (SOFTMAX) {
             w = expf(l - top);
         } else {
             const float t = expf(-__builtin_fabsf(l));  // the other way round, exp(-l) overflows below -88
-            w = (l < 0.0f ? t : 1.0f) / (1.0f + t);
+            w = (l < 0.0f ? expf(l - top) : 1.0f) / (1.0f + t);
         }
     }
     if (a.renormalize) {

@@ -31,9 +31,9 @@ extern "C" {
  * groups are taken: the groups of the largest max of rank (no bias) or sum of their two
  * largest ranks (with a bias).
  * Ranks with a bias are compared in float64, so that they are in the order of the formula
- * wherever that has one. NaN ranks before everything. Weights are float32. A row of only
- * -infinity gives weights 0 (softmax), as do chosen weights that sum to 0 where they are
- * renormalized; NaN or +infinity in a row makes softmax weights NaN.
+ * wherever that has one. NaN ranks before everything. Weights are float32; renormalized, they are
+ * the quotients of the scores however small these are, down to exp(-745), and 0 where all of them are
+ * below that (logits of -infinity, or of the lowest finite value). A row of only -infinity gives softmax weights 0; NaN or +infinity in a row makes softmax weights NaN.
  * One kernel. 1 <= E <= 1024, groups <= 64 divides E, 1 <= kept <= groups,
  * 1 <= k <= 64 and k <= kept * E / groups, scale finite.
  */

@@ -147,6 +147,39 @@ def test_route_small_sigmoids(skg):  # noqa: F811
     assert torch.equal(ids.cpu(), want) and ((w.double().cpu() - wref).abs() <= 2.0 ** -11 * wref).all()
 
 
+@pytest.mark.parametrize("depth", (85.0, 100.0, 120.0, 300.0, 600.0))
+def test_route_weights_far_below_the_top(skg, depth):  # noqa: F811
+    """Renormalized weights are quotients of the scores however small these are: float32 holds
+    none of exp(-120)."""
+    logits = -depth + torch.rand(9, 70, generator=gen(4), device="cuda")
+    check_route(skg, logits, 6, "sigmoid", scale=2.5)
+    logits[3:, 11] = -depth + 3.0
+    logits[6:, 69] = 0.0                       # the softmax's top
+    check_route(skg, logits, 6, "sigmoid")
+    bias = torch.rand(70, generator=gen(5), device="cuda")
+    bias[69] = -10.0                           # is not chosen
+    for score in ("softmax", "sigmoid"):
+        check_route(skg, logits, 6, score, bias)
+        check_route(skg, logits, 6, score, bias, 7, 3)
+    logits[:, :40] = -math.inf
+    for score in ("softmax", "sigmoid"):
+        check_route(skg, logits, 64, score, bias)
+
+
+@pytest.mark.parametrize("mask", (-math.inf, torch.finfo(torch.float32).min, -1e4))
+def test_route_of_masked_choices(skg, mask):  # noqa: F811
+    """Where every chosen expert is masked the weights are 0, also below a finite top."""
+    logits = torch.full((3, 32), mask, device="cuda")
+    logits[1:, 31] = 4.0
+    bias = torch.zeros(32, device="cuda")
+    bias[31] = -20.0
+    for score in ("softmax", "sigmoid"):
+        ids, w = skg.route(logits, 5, score, bias)
+        assert ids.tolist() == [[0, 1, 2, 3, 4]] * 3
+        # the softmax of a row of one finite value is even
+        assert (w[1:] == 0).all() and ((w[0] - 0.2).abs() < 1e-7 if score == "softmax" and mask > -math.inf else w[0] == 0).all()
+
+
 def test_route_strides_and_shapes(skg, ops):  # noqa: F811
     flat, view = walled(7, 96, 131, torch.float32)
     view.copy_(torch.randn(7, 96, generator=gen(1), device="cuda"))
