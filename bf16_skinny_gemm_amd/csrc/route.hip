@@ -245,7 +245,12 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a)
         // exponential of the largest chosen logit, leaves the quotients first. Below exp(-745),
         // the least of float64, scores are 0: masks of the lowest finite value leave nothing,
         // as those of -infinity.
-        const float most = value_of(wave_max(lane < a.k ? order_of(l) : 0u)), below = SOFTMAX ? most - top : most;
+        float most;
+        if constexpr (BIAS)
+            most = value_of(wave_max(lane < a.k ? order_of(l) : 0u));
+        else  // the first choice
+            most = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, l)));
+        const float below = SOFTMAX ? most - top : most;
         if (below >= -745.0f && below <= 0.0f)
             top = most;
     }
