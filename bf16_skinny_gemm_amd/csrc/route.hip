@@ -266,6 +266,8 @@ __global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a)
     if (a.renormalize) {
         const float all = wave_add(w);
         w = all == 0.0f ? 0.0f : w / all;
+        if constexpr (SOFTMAX && BIAS)  // NaN in the row, which need not be among the chosen
+            w = sum != sum ? sum : w;
     } else if constexpr (SOFTMAX) {
         w = sum == 0.0f ? 0.0f : w / sum;
     }

@@ -180,6 +180,20 @@ def test_route_of_masked_choices(skg, mask):  # noqa: F811
         assert (w[1:] == 0).all() and ((w[0] - 0.2).abs() < 1e-7 if score == "softmax" and mask > -math.inf else w[0] == 0).all()
 
 
+@pytest.mark.parametrize("groups,kept", ((1, 1), (8, 3)))
+@pytest.mark.parametrize("renormalize", (False, True))
+def test_route_of_rows_with_nan_and_a_bias(skg, renormalize, groups, kept):  # noqa: F811
+    """A NaN or +infinity anywhere in a row makes its softmax weights NaN, chosen or not."""
+    logits = torch.randn(5, 96, generator=gen(3), device="cuda")
+    logits[1, 95] = math.nan
+    logits[2, 40] = math.inf
+    logits[3] = -math.inf
+    logits[3, 90] = math.nan
+    bias = torch.linspace(1.0, -1.0, 96, device="cuda")
+    _, w = skg.route(logits, 4, "softmax", bias, groups, kept, renormalize)
+    assert w[1:4].isnan().all() and w[[0, 4]].isfinite().all()
+
+
 def test_route_strides_and_shapes(skg, ops):  # noqa: F811
     flat, view = walled(7, 96, 131, torch.float32)
     view.copy_(torch.randn(7, 96, generator=gen(1), device="cuda"))
