@@ -528,10 +528,7 @@ __global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
                     uint16_t *at = a.h + (int64_t)(first + r) * a.I * (split_h(BM) ? 2 : 1) + f;
                     *reinterpret_cast<u32x2 *>(at) = hi;
                     if constexpr (split_h(BM)) {
-                        const f32x4 w = widen4(hi);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)  // of an infinity nothing is left
-                            z[e] = __builtin_fabsf(w[e]) == __builtin_inff() ? 0.0f : z[e] - w[e];
+                        z -= widen4(hi);
                         *reinterpret_cast<u32x2 *>(at + a.I) = u32x2{pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3])};
                     }
                 }
@@ -820,8 +817,12 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
                 for (int i = 0; i < TM; ++i) {
                     if constexpr (SPLIT)  // both parts of h, in the columns up to 7
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[i][e] += __shfl_xor(acc[i][e], 8, 64);
+                        for (int e = 0; e < 4; ++e) {
+                            // where the first part's sum is infinite or NaN, it is all: what the second
+                            // one has of an infinite weight or h is NaN, or has another sign
+                            const float rest = __shfl_xor(acc[i][e], 8, 64);
+                            acc[i][e] += __builtin_fabsf(acc[i][e]) < __builtin_inff() ? rest : 0.0f;
+                        }
                     const bool live = i * 16 + i16 < pairs;
                     const int token = (int)entry[i][0];
                     const unsigned weight = entry[i][1];  // a bit_cast of the element itself takes the first one

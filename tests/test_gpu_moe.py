@@ -439,6 +439,29 @@ def test_experts_of_infinite_h(skg, M, E, H):  # noqa: F811
     assert y[:, 2:].isnan().all()  # infinity times zero
 
 
+@pytest.mark.parametrize("M,E,H", [(2, 16, 64), (12, 16, 64), (30, 6, 64), (40, 2, 64), (100, 16, 64), (2, 16, 60)])
+def test_experts_of_infinite_weights(skg, M, E, H):  # noqa: F811
+    """An infinite weight makes its output infinite whatever is left of h behind its first part: nothing
+    (the even features), as much as the sign of h, and of the other sign."""
+    I = 32
+    x = torch.zeros(M, H, device="cuda")
+    x[:, :2] = 1.0
+    gate, up = torch.zeros(E, I, H, device="cuda"), torch.zeros(E, I, H, device="cuda")
+    gate[:, :, 0] = 1.0
+    up[:, :, 0] = 1.0
+    up[:, 1::4, 1], up[:, 3::4, 1] = 2.0 ** -10, -2.0 ** -10
+    up[:, 31] = 0.0                              # h is 0
+    down = torch.full((E, H, I), 0.5, device="cuda")
+    for n in range(H):
+        down[:, n, n % I] = math.inf if n < I else -math.inf
+    ids = torch.arange(M, device="cuda").remainder(E).to(torch.int32)[:, None]
+    w = [v.to(torch.bfloat16) for v in (gate, up, down)]
+    y = skg.experts(x.to(torch.bfloat16), ids, torch.ones(M, 1, device="cuda"), *w, act="none").float()
+    n = torch.arange(H, device="cuda")
+    assert y[:, n % I == 31].isnan().all()       # 0 times infinity
+    assert (y[:, (n % I < 31) & (n < I)] == math.inf).all() and (y[:, (n % I < 31) & (n >= I)] == -math.inf).all()
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_experts_outputs_of_several_blocks(skg, kind):  # noqa: F811
     """Sets of outputs that two and many blocks share, and blocks of several sets."""
