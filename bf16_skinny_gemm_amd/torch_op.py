@@ -220,6 +220,14 @@ def _experts_py(x, ids, weights, w_gate, w_up, w_down, gate_scale=None, up_scale
                          None if residual is None else residual.reshape(M, H), act).reshape(x.shape)
 
 
+def _of(x, dtype):
+    """x, where it has the operator's type: the helpers go by the type of x."""
+    if x.dtype != dtype:
+        raise ValueError(f"x must be {dtype}, got {x.dtype}")
+    return x
+
+
+_E4M3 = torch.float8_e4m3fn
 _PY_KERNELS = {
     "rms_norm": lambda x, w, eps: _norm_py(x, w, eps),
     "add_rms_norm": lambda x, r, w, eps: _norm_py(x, w, eps, r),
@@ -229,9 +237,9 @@ _PY_KERNELS = {
     "linear_gated": lambda x, w, u, b=None, bu=None, act="silu", f32=False: _linear_py(
         x, w, b, None, act, f32, u, bu),
     "linear_fp8": lambda x, xs, w, ws, b=None, r=None, act="none", f32=False: _linear_py(
-        x, w, b, r, act, f32, x_scale=xs, w_scale=ws),
+        _of(x, _E4M3), w, b, r, act, f32, x_scale=xs, w_scale=ws),
     "linear_gated_fp8": lambda x, xs, w, ws, u, us, b=None, bu=None, act="silu", f32=False: _linear_py(
-        x, w, b, None, act, f32, u, bu, xs, ws, us),
+        _of(x, _E4M3), w, b, None, act, f32, u, bu, xs, ws, us),
 }
 # of the 8-bit integer operators, the router and the experts
 _PY_KERNELS_MORE = {
@@ -239,18 +247,12 @@ _PY_KERNELS_MORE = {
     "rms_norm_int8": lambda x, w, eps: _norm_py(x, w, eps, None, "int8"),
     "add_rms_norm_int8": lambda x, r, w, eps: _norm_py(x, w, eps, r, "int8"),
     "linear_int8": lambda x, xs, w, ws, b=None, r=None, act="none", f32=False: _linear_py(
-        _int8(x), w, b, r, act, f32, x_scale=xs, w_scale=ws),
+        _of(x, torch.int8), w, b, r, act, f32, x_scale=xs, w_scale=ws),
     "linear_gated_int8": lambda x, xs, w, ws, u, us, b=None, bu=None, act="silu", f32=False: _linear_py(
-        _int8(x), w, b, None, act, f32, u, bu, xs, ws, us),
+        _of(x, torch.int8), w, b, None, act, f32, u, bu, xs, ws, us),
     "route": _route_py,
     "experts": _experts_py,
 }
-
-
-def _int8(x):
-    if x.dtype != torch.int8:
-        raise ValueError(f"x must be int8, got {x.dtype}")
-    return x
 
 
 def _refuse_cpu(name):

@@ -152,3 +152,17 @@ def test_operators_refuse_cpu_tensors_and_give_shapes_to_a_tracer(skg):  # noqa:
             continue
         assert [(tuple(g.shape), g.dtype) for g in got] == [
             ((2, 3, 32), torch.int8), ((2, 3), torch.float32), ((2, 3, 32), torch.bfloat16)][:len(got)]
+
+
+def test_python_kernels_take_their_own_type(skg):  # noqa: F811
+    """Those of the e4m3 projections refuse 8-bit integers, and the other way round, as the C++ ones do."""
+    from bf16_skinny_gemm_amd import torch_op as t
+
+    s, ws = torch.ones(2), torch.ones(8)
+    for kernels, name, other in ((t._PY_KERNELS, "fp8", torch.int8), (t._PY_KERNELS_MORE, "int8", torch.float8_e4m3fn)):
+        for dtype in (other, torch.bfloat16):
+            x, w = torch.zeros(2, 16, dtype=dtype), torch.zeros(8, 16, dtype=dtype)
+            with pytest.raises(ValueError, match="x must be torch"):
+                kernels["linear_" + name](x, s, w, ws)
+            with pytest.raises(ValueError, match="x must be torch"):
+                kernels["linear_gated_" + name](x, s, w, ws, w, ws)
