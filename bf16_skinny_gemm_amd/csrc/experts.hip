@@ -31,12 +31,11 @@
 // blocks that the hardware hands out, and gain all others up to half.
 #include "ops_host.hpp"
 
-#include <cmath>
 #include <cstdint>
 
+#include "experts_plan.hpp"
 #include "lds_load.hpp"
 #include "linear.hpp"
-#include "validate_moe.hpp"
 
 namespace skg {
 
@@ -76,8 +75,7 @@ struct ExpertArgs {
     Divisor by_k, by_grid, by_features, by_up, by_down;  // k, blocks, I / 8, the stages of H and of I
 };
 
-constexpr int kMostPairs = skg_host::kExpertsRows * skg_host::kMaxExpertsK;  // 4096: 12 bits and one
-constexpr int kMostTiles = skg_host::kMaxExperts + kMostPairs / 4;
+using skg_host::kMostPairs, skg_host::kMostTiles, skg_host::split_h, skg_host::h_rows;
 static_assert(skg_host::kMaxExperts <= 1 << 10 && kMostPairs <= 1 << 15, "a tile is one word");
 
 // Sixteen 8-bit integers as bfloat16.
@@ -106,10 +104,8 @@ __device__ __forceinline__ void widen_weight(const u32x4 &v, u32x4 &lo, u32x4 &h
         widen(v, lo, hi);
 }
 
-// x (or h) of a stage lies in PLANES planes of [rows][128 bytes], a column of weights beside
-// the same column of x: the 16 bytes of an 8-bit weight beside two pieces of 16 bytes.
 template <int TYPE>
-constexpr int planes() { return TYPE == kWBf16 ? 1 : 2; }
+constexpr int planes() { return skg_host::planes_of(TYPE); }
 
 // One fragment of weights (the lane's pieces g and g + 4 of its row), widened.
 template <int TYPE>
@@ -147,32 +143,17 @@ __device__ __forceinline__ void read_x(const uint8_t *at, int row, int plane, in
     }
 }
 
-// Tiles of up to 8 rows leave half of the instruction's 16 columns free. There h is held as two
-// bfloat16 values, the rounded one and what it leaves, in the columns 0..7 and 8..15: 16 bits of
-// it for no product more, where one rounding of it would be as large an error as that of y. It
-// costs nothing with 4 rows, and 6 us of 96 with 8 (37 tokens, 16 experts of 4096 x 1536,
-// bfloat16), where a compute unit takes in as much of h as of the weights. Tiles of more rows
-// hold h in one bfloat16 value, as a projection of its own would store it: two would double
-// the products and loads, and the many pairs average the error of each out.
-constexpr bool split_h(int rows) { return rows <= 8; }
-constexpr int h_rows(int rows) { return split_h(rows) ? 2 * rows : rows; }
-
-// Bytes of a stage: weights, x or h, and what belongs to them.
-template <int TYPE, int BM, bool RESIDENT>
-constexpr int up_stage() { return 2048 + (RESIDENT ? 0 : planes<TYPE>() * BM * 128) + (TYPE == kWBf16 ? 0 : 64); }
-template <int TYPE, int BM>
-constexpr int down_stage() { return 2048 + planes<TYPE>() * h_rows(BM) * 128 + BM * 16 + (TYPE == kWBf16 ? 0 : 64); }
-
 // ---- the pairs by expert -----------------------------------------------------------
 
 // The plan of a pass in LDS, made by every block for itself: the tiles (expert | pairs << 10 |
 // first pair << 16) and each sorted pair's token.
 template <bool WAVE>
 struct Plan {
-    unsigned tiles[WAVE ? 64 : kMostTiles];
-    uint8_t tokens[WAVE ? 64 : kMostPairs];
+    unsigned tiles[WAVE ? skg_host::kWavePairs : kMostTiles];
+    uint8_t tokens[WAVE ? skg_host::kWavePairs : kMostPairs];
     int count;
 };
+static_assert(sizeof(Plan<true>) == skg_host::plan_bytes(true) && sizeof(Plan<false>) == skg_host::plan_bytes(false), "in LDS");
 
 // What making it takes beside: which tokens name an expert, and where its pairs start.
 struct Scratch {
@@ -383,7 +364,7 @@ __global__ __launch_bounds__(WAVES * 64) void experts_up_kernel(ExpertArgs a)
     constexpr int PLANES = planes<TYPE>();
     constexpr int TM = (BM + 15) / 16, XR = (BM + 7) / 8;
     constexpr int XAT = 16 * 128, XPLANE = BM * 128, SAT = XAT + (RESIDENT ? 0 : PLANES * XPLANE);
-    constexpr int STAGE = up_stage<TYPE, BM, RESIDENT>();
+    constexpr int STAGE = skg_host::up_stage(TYPE, BM, RESIDENT);
     constexpr int LOADS = 2 + (RESIDENT ? 0 : PLANES * BM / 8) + (TYPE == kWBf16 ? 0 : 2);
     constexpr int RINGS = WAVES * RING * STAGE, ROOM = RINGS + (RESIDENT ? XROOM : 0);
     constexpr int SMEM = !WAVE && (int)sizeof(Scratch) > ROOM ? (int)sizeof(Scratch) : ROOM;
@@ -649,7 +630,7 @@ __global__ __launch_bounds__(WAVES * 64) void experts_down_kernel(ExpertArgs a, 
     constexpr bool SPLIT = split_h(BM);
     constexpr int HR = h_rows(BM);  // rows of h in LDS: split, those of the first values, then the others
     constexpr int XAT = 2048, XPLANE = HR * 128, EAT = XAT + PLANES * XPLANE, SAT = EAT + BM * 16;
-    constexpr int STAGE = down_stage<TYPE, BM>();
+    constexpr int STAGE = skg_host::down_stage(TYPE, BM);
     constexpr int HLOADS = PLANES * HR / 8;  // 8 rows each
     constexpr int LOADS = 2 + HLOADS + 1 + (TYPE == kWBf16 ? 0 : 1);
     constexpr int OUTS = MC * 16;  // floats of a wave
@@ -999,66 +980,40 @@ __global__ __launch_bounds__(256) void experts_down_any_kernel(ExpertArgs a)
 namespace skg_host {
 namespace {
 
-// The kernels for one tile height: the first, for pairs of one wave or more, with x in LDS or
-// not (and the room that it takes), and the second, by the tokens that it has room for: up to
-// 16, 64 or 128.
-struct UpKernel {
-    const void *fn;
-    int waves, room;
-};
-
-constexpr int kLds = 163840;
-
-// As many stages as fit, 6 at most.
-constexpr int ring_of(int bytes, int waves, int stage) { return bytes / (waves * stage) < 6 ? bytes / (waves * stage) : 6; }
-
 template <int TYPE, int BM, bool WAVE, int RING>
-UpKernel up_resident()
+const void *up_resident_fn()
 {
-    constexpr int ROOM = (kLds - (int)sizeof(skg::Plan<WAVE>) - 64 - RING * 8 * skg::up_stage<TYPE, BM, true>()) / 1024 * 1024;
-    return UpKernel{(const void *)&skg::experts_up_kernel<TYPE, BM, RING, 8, WAVE, true, ROOM>, 8, ROOM};
+    constexpr UpPlan U = up_resident(TYPE, BM, WAVE, RING);
+    return (const void *)&skg::experts_up_kernel<TYPE, BM, U.ring, U.waves, WAVE, true, U.room>;
 }
 
+// The first kernel of a plan that up_plan() made for tiles of BM rows.
 template <int TYPE, int BM, bool WAVE>
-UpKernel up_streamed()
+const void *up_fn(const UpPlan &u)
 {
-    constexpr int B = BM == 4 ? 8 : BM, WAVES = BM == 32 && TYPE != skg::kWBf16 ? 4 : 8;
-    constexpr int RING = ring_of(kLds - (int)sizeof(skg::Plan<WAVE>) - 64, WAVES, skg::up_stage<TYPE, B, false>());
-    return UpKernel{(const void *)&skg::experts_up_kernel<TYPE, B, RING, WAVES, WAVE, false, 0>, WAVES, 0};
+    if constexpr (resident_offered(TYPE, BM, WAVE))
+        if (u.room)
+            return u.ring == kResidentRings[0]   ? up_resident_fn<TYPE, BM, WAVE, kResidentRings[0]>()
+                   : u.ring == kResidentRings[1] ? up_resident_fn<TYPE, BM, WAVE, kResidentRings[1]>()
+                                                 : up_resident_fn<TYPE, BM, WAVE, kResidentRings[2]>();
+    constexpr UpPlan U = up_streamed(TYPE, BM, WAVE);
+    return (const void *)&skg::experts_up_kernel<TYPE, U.rows, U.ring, U.waves, WAVE, false, 0>;
 }
 
-// The first kernel for rows of `xbytes` bytes of x.
-template <int TYPE, int BM, bool WAVE>
-UpKernel up_kernel(int64_t xbytes)
+template <int TYPE, int BM, int TOKENS>
+const void *down_fn_of()
 {
-    if constexpr (BM < 32 || TYPE == skg::kWBf16 || !WAVE) {  // 8-bit weights, 32 rows and 64 pairs: x is wide
-        static const UpKernel k[] = {up_resident<TYPE, BM, WAVE, 6>(), up_resident<TYPE, BM, WAVE, 4>(),
-                                     up_resident<TYPE, BM, WAVE, 3>()};
-        for (const UpKernel &u : k)
-            if ((xbytes + 255) / 256 * 256 * BM <= u.room)
-                return u;
-    }
-    return up_streamed<TYPE, BM, WAVE>();
-}
-
-struct DownKernel {
-    const void *fn;
-    int waves;
-};
-
-template <int TYPE, int BM, int MC>
-DownKernel down_of()
-{
-    constexpr int WAVES = MC == 128 || (BM == 32 && TYPE != skg::kWBf16) ? 4 : 8;
-    constexpr int RING = ring_of(kLds - 4 * skg::kMostTiles - 16 - WAVES * MC * 64, WAVES, skg::down_stage<TYPE, BM>());
-    return DownKernel{(const void *)&skg::experts_down_kernel<TYPE, BM, RING, WAVES, MC>, WAVES};
+    constexpr DownPlan D = down_of(TYPE, BM, TOKENS);
+    return (const void *)&skg::experts_down_kernel<TYPE, BM, D.ring, D.waves, TOKENS>;
 }
 
 template <int TYPE, int BM>
-DownKernel down_kernel(int M)
+const void *down_fn(const DownPlan &d)
 {
     // tiles of 32 rows are for more than 16 tokens
-    return M <= 16 ? down_of<TYPE, BM == 32 ? 16 : BM, 16>() : M <= 64 ? down_of<TYPE, BM, 64>() : down_of<TYPE, BM, 128>();
+    return d.tokens == 16   ? down_fn_of<TYPE, BM == 32 ? 16 : BM, 16>()
+           : d.tokens == 64 ? down_fn_of<TYPE, BM, 64>()
+                            : down_fn_of<TYPE, BM, 128>();
 }
 
 skg::Divisor divisor(unsigned d)
@@ -1087,10 +1042,9 @@ template <int TYPE, int BM>
 int run_rows(skg::ExpertArgs &a, int cus, hipStream_t stream)
 {
     const int P = a.M * a.k;
-    const int64_t xbytes = 2 * (int64_t)a.H;
-    const UpKernel up = P <= 64 ? up_kernel<TYPE, BM, true>(xbytes) : up_kernel<TYPE, BM, false>(xbytes);
-    const int height = up.room ? BM : BM < 8 ? 8 : BM;
-    int most = a.E + P / height;  // tiles, at most
+    const bool wave = P <= kWavePairs;
+    const UpPlan up = up_plan(TYPE, BM, wave, a.H);
+    int most = a.E + P / up.rows;  // tiles, at most
     most = P < most ? P : most;
     // the kernels count units and stages in 32 bits
     const int64_t features = ((int64_t)a.I + 7) / 8, sets = ((int64_t)a.H + 15) / 16, per = skg::per_stage(TYPE);
@@ -1102,11 +1056,13 @@ int run_rows(skg::ExpertArgs &a, int cus, hipStream_t stream)
     a.by_up = divisor((unsigned)up_stages);
     a.by_down = divisor((unsigned)down_stages);
     void *args[] = {&a, &most};
-    const int st = ops_launch(up.fn, dim3((unsigned)cus), up.waves * 64, args, stream);
+    const int st = ops_launch(wave ? up_fn<TYPE, BM, true>(up) : up_fn<TYPE, BM, false>(up), dim3((unsigned)cus), up.waves * 64,
+                              args, stream);
     if (st != SKINNY_OK)
         return st;
-    const DownKernel down = height == BM ? down_kernel<TYPE, BM>(a.M) : down_kernel<TYPE, 8>(a.M);
-    return ops_launch(down.fn, dim3((unsigned)kDownBlocks), down.waves * 64, args, stream);
+    const DownPlan down = down_of(TYPE, up.rows, tokens_room(a.M));
+    return ops_launch(up.rows == BM ? down_fn<TYPE, BM>(down) : down_fn<TYPE, 8>(down), dim3((unsigned)kDownBlocks),
+                      down.waves * 64, args, stream);
 }
 
 template <int TYPE>
@@ -1115,20 +1071,7 @@ int run_type(const skg::ExpertArgs &a, bool vector, int cus, hipStream_t stream)
     skg::ExpertArgs args = a;
     if (!vector)
         return run_any<TYPE>(args, stream);
-    const int P = a.M * a.k;
-    // pairs of an expert that has any, were the pairs spread evenly
-    const double some = a.E * (1.0 - std::pow(1.0 - 1.0 / a.E, P)), even = P / some;
-    // A tile's rows of x (or h) cost LDS and loads whether there are pairs for them or not, and an
-    // expert with more pairs than rows is read again, from the caches at best. With narrow x,
-    // 16 rows of it stay in LDS. Both kernels, in microseconds, with 8 and with 16 rows:
-    // 61 tokens, 64 experts of 2048 x 1408, int8 (5.7 pairs each) 129 and 107; 32 tokens, 64 of
-    // 4096 x 1024, e4m3 (2.4) 116 and 124, with 4 rows 121, and (4.1) 147 and 150, with 4 rows 185.
-    // With 16 and with 32: 100 tokens, 64 of 4096 x 1024,
-    // int8 (12.5) 221 and 267; 128 tokens, 8 of 4096 x 1536, int8 (32) 96 and 79, 8 of
-    // 2048 x 1024 (64) 59 and 62; 128 tokens, 64 of 4096 x 1024, bfloat16 (20) 539 and 365.
-    const bool bytes = TYPE != skg::kWBf16, narrow = a.H <= 2560;
-    const double eight = narrow ? 4.5 : 7.0, sixteen = bytes ? (narrow ? 64.0 : 20.0) : narrow ? 14.0 : 11.0;
-    const int rows = even <= 2.0 ? 4 : even <= eight ? 8 : even <= sixteen || a.M <= 16 ? 16 : 32;
+    const int rows = tile_rows(TYPE, a.M, a.E, a.k, a.H);
     return rows == 4    ? run_rows<TYPE, 4>(args, cus, stream)
            : rows == 8  ? run_rows<TYPE, 8>(args, cus, stream)
            : rows == 16 ? run_rows<TYPE, 16>(args, cus, stream)

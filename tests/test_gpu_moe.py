@@ -13,6 +13,7 @@ import math
 import pytest
 import torch
 
+from .experts_choices import CHOICES
 from .test_gpu_ops import BF16, F32, act_ref, bits, filled, gen, ops, skg, walled, walls_hold  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -409,6 +410,15 @@ def test_experts_tiles(skg, rows, kind):  # noqa: F811
             check_experts(skg, M, E, k, H, 64, kind, ids=ids, residual=True, seed=H + M)
             if H < 1000:
                 check_experts(skg, M, E, k, 80, H, kind, ids=ids, seed=H + M)
+
+
+@pytest.mark.parametrize("kind", range(4))
+def test_experts_every_kernel(skg, kind):  # noqa: F811
+    """Every kernel that calls choose among, first and second (which of them: test_experts_choice)."""
+    for kinds, sizes in CHOICES.items():
+        for i, (M, E, k, H) in enumerate(sizes if kind in kinds else ()):
+            ids = torch.zeros(M, k, dtype=torch.int32, device="cuda") if k > E else None
+            check_experts(skg, M, E, k, H, 80, KINDS[kind], ids=ids, residual=i % 2 == 0, seed=M + H)
 
 
 @pytest.mark.parametrize("kind", KINDS)
