@@ -894,7 +894,9 @@ def experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w_gate: t
     scales per 128 x 128 block ([E, ceil(I/128), ceil(H/128)], [E, ceil(H/128), ceil(I/128)]). Parts
     [e] must be contiguous; the two halves of a merged [E, 2 I, H] weight are taken as views.
     Two kernel launches for every 128 rows on the current stream; for up to some hundred rows.
-    out (which may be the residual) and workspace (from experts_workspace) may be given."""
+    act(..) * (..) is rounded to bfloat16 in batches that give an expert more than a few rows, and
+    held in 16 bits else, so a row's last bits depend on the batch. out (which may be the residual)
+    and workspace (from experts_workspace) may be given."""
     ldx = _matrix(x, "x", torch.bfloat16, None)
     M, H = x.shape
     if act not in ACTS:

@@ -24,7 +24,11 @@
 // What it measured, cold weights, both kernels by the trace (least of 36): one token, 8 experts of
 // 4096 x 1024 in bfloat16 22.9 + 13.1 us (5.6 TB/s); 5 tokens, 8 of 288 experts of that size
 // with block scales 52.4 + 27.8 (5.9); 61 tokens, 6 of 64 of 2048 x 1408 in int8 61.6 + 44.5
-// (5.2); 37 tokens, 2 of 16 of 4096 x 1536 in bfloat16 61.2 + 38.3 (6.0). So HBM bounds them.
+// (5.2); 37 tokens, 2 of 16 of 4096 x 1536 in bfloat16 61.2 + 38.3 (6.0). Reads alone reach 6.8 TB/s
+// on this card: HBM bounds the first kernel and the second one in bfloat16. With 8-bit weights
+// and 16 rows the second one has 4.1 TB/s: a block takes in twice as many bytes of h as of the weights, in a
+// ring of two stages, and its reads of h meet in the banks of LDS (0.33 of the active cycles,
+// 0.25 to 0.37 in all kernels of 8-bit weights, 0.02 at most in those of bfloat16).
 // Three tokens, 4 of 64 of 2048 x 768 with row scales take 12.4 + 10.4 (2.3 TB/s): an empty
 // launch of the first kernel, with its plan, is 2.2 to 4 us and of the second 4, and each wave
 // has 9 stages, fewer than two rings. Equal runs cost the largest calls of few tokens 3% against

@@ -31,7 +31,7 @@
 // 1430 TF), 107 to 118 with residual, activation and cold inputs; e4m3 with row scales
 // 4096 x 4096 x 8192 in 92 to 97 (2830 to 2990 TF), 101 to 108 with bias, residual and cold
 // inputs. 8-bit integers are at the same rate: 4095 x 4096 x 8192 with bias and residual in
-// 103 to 107, and exact. With block scales, where each product has four multiply-adds behind it and no tile is
+// 102 to 109, and exact. With block scales, where each product has four multiply-adds behind it and no tile is
 // larger than 256 x 128, 4096^3 takes 74 to 78 against 51 to 53. For float32 outputs of
 // 8-bit inputs both operands are widened at every use: 4096 x 4096 x 8192 307 to 318 with row
 // scales, 339 to 353 with block scales. At the tiles of 128 x 128, by what a compute unit

@@ -12,7 +12,7 @@
 // the scale instead of being dropped by a float maximum.
 //
 // Rows as they are to 8-bit integers: 100 x 8192 in 2.4 us; the norm of 4 x 4096 with a residual
-// in 2.7, the launch.
+// in 2.8, the launch; 8192 x 4096 rows 19.1, their norm 22.9, with a residual 40.1 (5.3, 4.4 and 5.9 TB/s).
 #include "ops_host.hpp"
 
 #include <atomic>

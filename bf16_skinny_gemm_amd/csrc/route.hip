@@ -9,12 +9,13 @@
 // exact: in float32 two experts whose scores lie within a rounding of each other would
 // change places, and so the choice.
 //
-// A prompt is bound by instructions, one token by the launch: of 4.4 us for 1 x 288, k 8, the
-// empty kernel is 2. 8191 x 256, sigmoid, k 8: the logits alone 8.4 us (1.1 TB/s), most of it
-// the eight rounds of the wave's maximum; with a bias 13.0, of which float64's exponentials and
-// quotients are the 4.6; with four of eight groups 16.5 (one lane a group: 18.1). A ranking
-// in float32 that goes to float64 only where two ranks lie close gained 8% and was not worth
-// its second path.
+// A prompt is bound by instructions, one token by the launch: of 4.5 us for 1 x 288, k 8, the
+// empty kernel is 2. 8191 x 256, sigmoid, k 8, calls back to back: the logits alone 7.9 us
+// (1.1 TB/s), most of it the eight rounds, each a maximum over the wave for one token's four values a
+// lane; with a bias 13.2, of which float64's exponentials and quotients are the 5; with four of
+// eight groups 17.5 (one lane a group: a tenth more). A ranking in float32 that goes to float64
+// only where two ranks lie close gained 8% and was not worth its second path. Several tokens
+// a wave would share the rounds' steps; that is not built.
 #include "ops_host.hpp"
 
 #include <cstdint>

@@ -76,9 +76,10 @@ int skinny_rms_norm_fp8(const skinny_norm_t *args, hipStream_t stream);
 
 /* y as 8-bit integers with a float32 scale per row (group 0): scale = max(largest |y|, 2^-100)
  * / 127 and q = y / scale rounded to the nearest integer, ties to even, so -127 .. 127. The
- * quotient is float32's, correctly rounded (here not the product with a reciprocal): values half
- * way between two integers, up to the rounding of the scale, go where a division puts them. Rows
- * of zeros give zeros; a NaN or an infinity in a row makes its
+ * quotient is that of a float32 division here, not the product with a reciprocal, so values half
+ * way between two integers, up to the rounding of the scale, go where the division puts them
+ * (for all rows of skinny_quantize_int8; here y may lie within 2^-22 of a step's last bit of a tie
+ * of the division itself). Rows of zeros give zeros; a NaN or an infinity in a row makes its
  * scale NaN and its q 0, so that q * scale is NaN. */
 int skinny_rms_norm_int8(const skinny_norm_t *args, hipStream_t stream);
 
